@@ -15,11 +15,20 @@
  *                       `mamba3_siso` / `mamba3_mimo` in one call
  *   m3_siso_backward  - `mamba3_siso_backward` (the eleven SISO adjoints)
  *   m3_mimo_backward  - `mamba3_mimo_backward` (the fifteen MIMO adjoints)
+ * Operators of the linear-attention layers that hybrid models put between
+ * selective-state layers (no counterpart on the pages):
+ *   m3_qk_norm_rope   - norm of each query and key head with the position
+ *                       rotation in the same pass; m3_qk_norm_rope_backward
+ *   m3_linear_attention_forward / _step / _backward - linear attention with a
+ *                       decay per head: prompts, single tokens, adjoints
  *
  * Conventions for every entry point:
  *  - Every tensor is float32, dense row-major, in device memory owned by the
  *    caller; the library allocates nothing and keeps no pointer after return.
- *  - Every base pointer must be 16-byte aligned (M3_ERR_UNALIGNED otherwise).
+ *    (The activations of the linear-attention operators also come as bfloat16
+ *    and with a row stride: see m3_dtype and their config structs.)
+ *  - Every base pointer must be 16-byte aligned (M3_ERR_UNALIGNED otherwise);
+ *    strided activations need only their element's alignment.
  *  - All checks run on the host before anything is enqueued. A rejected call
  *    enqueues no work and leaves every output and state buffer untouched.
  *  - Work is enqueued on `stream` (a cudaStream_t; NULL is the legacy default
@@ -390,6 +399,157 @@ int m3_mimo_step(const m3_ssm_config* cfg, const float* c, const float* b, const
                  const float* mimo_x, const float* mimo_z, const float* mimo_o,
                  const float* norm_weight, float* ssm_state, float* angle_state,
                  float* k_state, float* v_state, float* out, m3_stream_t stream);
+
+/* Element type of the activations of the linear-attention operators. Norm
+ * weights, rotation tables, decays, states and weight gradients are float32. */
+enum m3_dtype { M3_DTYPE_FP32 = 0, M3_DTYPE_BF16 = 1 };
+
+/* Shape of m3_qk_norm_rope: `rows` tokens with num_q_heads query heads and
+ * num_k_heads key heads (either may be 0) of head_dim values, 1 <= head_dim <=
+ * 256; num_rope_angles A, 2A <= head_dim; tables of max_positions rows. A row
+ * of an operand starts *_stride elements after the one before it (0: dense,
+ * heads * head_dim), so queries and keys can be columns of a packed
+ * projection; the heads of a row are adjacent. */
+typedef struct {
+  int64_t rows;
+  int64_t num_q_heads;
+  int64_t num_k_heads;
+  int64_t head_dim;
+  int64_t num_rope_angles;
+  int64_t max_positions;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t q_out_stride;
+  int64_t k_out_stride;
+  float epsilon;
+  int32_t dtype; /* m3_dtype of q, k, their outputs and their gradients */
+} m3_qk_norm_rope_config;
+
+/*
+ * m3_qk_norm_rope - RMS norm of every query and key head, then the rotation by
+ * the token's position, in one pass:
+ *   u_d = x_d / sqrt(mean_e x_e^2 + epsilon) * weight_d
+ *   y_a = u_a cos - u_{a+A} sin, y_{a+A} = u_a sin + u_{a+A} cos   (a < A),
+ *   y_d = u_d                                                      (d >= 2A)
+ * with cos / sin = cos_table / sin_table [max_positions, A] at the row's
+ * position (the library's split-half pairing). q [rows, num_q_heads,
+ * head_dim], k [rows, num_k_heads, head_dim] and their outputs likewise; an
+ * output may be its input (same pointer and stride). q_weight, k_weight
+ * [head_dim] float32 (NULL: ones). positions [rows] int32 (NULL: the row
+ * number); a row whose position lies outside [0, max_positions) is normalised
+ * but not rotated. The tables may be NULL when A == 0. Sums in float32, one
+ * rounding at the output.
+ * Checks: rows >= 0, heads >= 0 and not both 0, the limits above, strides 0
+ * or >= heads * head_dim, epsilon finite and > 0, positions NULL only with
+ * rows <= max_positions.
+ */
+int m3_qk_norm_rope(const m3_qk_norm_rope_config* cfg, const void* q, const void* k,
+                    const float* q_weight, const float* k_weight, const float* cos_table,
+                    const float* sin_table, const int32_t* positions, void* q_out, void* k_out,
+                    m3_stream_t stream);
+
+/*
+ * m3_qk_norm_rope_backward - its adjoint. q, k are the inputs (strides of the
+ * config); grad_q_out / grad_k_out have the output strides, grad_q / grad_k
+ * are dense. With g the output gradient rotated back, s the inverse RMS and
+ * xh = s x:
+ *   grad_x_d = s (w_d g_d - xh_d mean_e(w_e g_e xh_e)),
+ *   grad_weight_d = sum over rows and heads of g_d xh_d  (float32, summed in a
+ *   fixed order: bit-identical from call to call).
+ * grad_q_weight / grad_k_weight may be NULL (not wanted). Workspace as
+ * m3_qk_norm_rope_backward_workspace() says.
+ */
+int m3_qk_norm_rope_backward_workspace(const m3_qk_norm_rope_config* cfg, size_t* bytes);
+int m3_qk_norm_rope_backward(const m3_qk_norm_rope_config* cfg, const void* q, const void* k,
+                             const float* q_weight, const float* k_weight,
+                             const float* cos_table, const float* sin_table,
+                             const int32_t* positions, const void* grad_q_out,
+                             const void* grad_k_out, void* grad_q, void* grad_k,
+                             float* grad_q_weight, float* grad_k_weight, void* workspace,
+                             size_t workspace_bytes, m3_stream_t stream);
+
+/* Shape of linear attention: batch_size sequences of up to sequence_length
+ * tokens in total_rows rows; num_heads H with values of head_dim P, queries
+ * and keys of state_size N shared by the H / G heads of each of num_groups G
+ * groups (0: one per head), 1 <= P, N <= 128. Row strides in elements as in
+ * m3_qk_norm_rope_config (0: dense). scale multiplies every output. num_slots
+ * is read by the step only. */
+typedef struct {
+  int64_t batch_size;
+  int64_t sequence_length;
+  int64_t total_rows;
+  int64_t num_heads;
+  int64_t num_groups;
+  int64_t head_dim;
+  int64_t state_size;
+  int64_t num_slots;
+  int64_t q_stride;
+  int64_t k_stride;
+  int64_t v_stride;
+  int64_t out_stride;
+  float scale;
+  int32_t dtype; /* m3_dtype of q, k, v, out and their gradients */
+} m3_linear_attention_config;
+
+/*
+ * m3_linear_attention_forward - causal linear attention with a decay per head
+ * over whole sequences (chunked form). With lam = exp(log_decay[h]):
+ *   S_t = lam S_{t-1} + v_t k_t^T,   out_t = scale S_t q_t,   S_{-1} = initial_state
+ * q, k [total_rows, G, N], v, out [total_rows, H, P]; log_decay [H] float32
+ * (0: no decay; -inf: only the token itself); initial_state, final_state
+ * [B, H, P, N] float32, each may be NULL (zero / not wanted) and they may be
+ * the same buffer.
+ * offsets NULL: sequence b is rows b * sequence_length .. (total_rows ==
+ * batch_size * sequence_length). offsets [batch_size + 1] int32, in device
+ * memory: sequence b is rows offsets[b] .. offsets[b + 1] (ascending, within
+ * total_rows; an offset outside is taken as the nearest row inside, and no
+ * sequence may be longer than sequence_length: its later rows are not
+ * computed). A sequence of length zero hands its initial state on. Rows of no
+ * sequence are not written.
+ * States and sums are float32; with bfloat16 activations the products take
+ * bfloat16 operands. A non-finite value reaches the outputs of its own
+ * 128-token chunk and of the tokens after it, never another sequence.
+ * Workspace (device scratch) as m3_linear_attention_forward_workspace() says;
+ * m3_workspace_status() reads its status word.
+ */
+int m3_linear_attention_forward_workspace(const m3_linear_attention_config* cfg, size_t* bytes);
+int m3_linear_attention_forward(const m3_linear_attention_config* cfg, const void* q,
+                                const void* k, const void* v, const float* log_decay,
+                                const int32_t* offsets, const float* initial_state, void* out,
+                                float* final_state, void* workspace, size_t workspace_bytes,
+                                m3_stream_t stream);
+
+/*
+ * m3_linear_attention_step - one token of every sequence: q, k [B, G, N], v,
+ * out [B, H, P], total_rows == batch_size, sequence_length == 1. The states
+ * [num_slots, H, P, N] float32 are updated in place. slots [B] int32, device
+ * memory: the state that each row reads and writes (no two rows the same); a
+ * row whose slot lies outside [0, num_slots) changes no state and gets a zero
+ * output. slots NULL: row b uses state b (num_slots 0, or >= batch_size).
+ */
+int m3_linear_attention_step(const m3_linear_attention_config* cfg, const void* q, const void* k,
+                             const void* v, const float* log_decay, const int32_t* slots,
+                             float* state, void* out, m3_stream_t stream);
+
+/*
+ * m3_linear_attention_backward - the adjoint of m3_linear_attention_forward:
+ *   grad_q_t = scale sum_{u<=t} lam^(t-u) (grad_out_t . v_u) k_u + scale lam^(t+1) initial_state^T grad_out_t
+ *   grad_k_t = scale sum_{u>=t} lam^(u-t) (v_t . grad_out_u) q_u + lam^(len-1-t) grad_final_state^T v_t
+ *   grad_v_t = scale sum_{u>=t} lam^(u-t) (k_t . q_u) grad_out_u + lam^(len-1-t) grad_final_state k_t
+ *   grad_initial_state = lam^len grad_final_state + scale sum_t lam^(t+1) grad_out_t q_t^T
+ * (grad_q, grad_k summed over the heads of a group, in head order). grad_out
+ * has out's stride; grad_q, grad_k, grad_v are dense. initial_state and
+ * grad_final_state may be NULL (zero), grad_initial_state NULL (not wanted).
+ * The decays are taken as fixed: they get no gradient.
+ */
+int m3_linear_attention_backward_workspace(const m3_linear_attention_config* cfg, size_t* bytes);
+int m3_linear_attention_backward(const m3_linear_attention_config* cfg, const void* grad_out,
+                                 const void* q, const void* k, const void* v,
+                                 const float* log_decay, const int32_t* offsets,
+                                 const float* initial_state, const float* grad_final_state,
+                                 void* grad_q, void* grad_k, void* grad_v,
+                                 float* grad_initial_state, void* workspace,
+                                 size_t workspace_bytes, m3_stream_t stream);
 
 /*
  * m3_workspace_status - waits for `stream`, then reads the device status word

@@ -2,7 +2,9 @@
 
 The product is the C-ABI library `libm3.so` (declared in include/m3.h):
 m3_preprocess, m3_siso_forward, m3_mimo_forward, m3_siso_step, m3_mimo_step,
-m3_siso_backward, m3_mimo_backward, m3_preprocess_backward.
+m3_siso_backward, m3_mimo_backward, m3_preprocess_backward, and the operators of
+linear-attention layers: m3_qk_norm_rope and m3_linear_attention_forward /
+_step / _backward.
 This package holds its CUDA sources (`csrc/`), the in-tree build (`build.py`),
 a ctypes binding with the same entry-point names (`_binding.py`), torch.autograd
 bindings that pair each scan with its adjoints (`autograd.py`) and the seeded
@@ -19,5 +21,10 @@ from ._binding import (  # noqa: F401
     m3_siso_step, m3_mimo_step, m3_workspace_status, LIB_PATH, m3_siso_prefill_workspace,
     m3_mimo_prefill_workspace, m3_siso_prefill, m3_mimo_prefill, m3_selftest_wait_timeout,
     m3_siso_backward_workspace, m3_siso_backward, m3_mimo_backward_workspace,
-    m3_mimo_backward, m3_preprocess_backward_workspace, m3_preprocess_backward)
+    m3_mimo_backward, m3_preprocess_backward_workspace, m3_preprocess_backward,
+    M3_DTYPE_FP32, M3_DTYPE_BF16, QkNormRopeConfig, LinearAttentionConfig, qk_norm_rope_config,
+    linear_attention_config, m3_qk_norm_rope, m3_qk_norm_rope_backward_workspace,
+    m3_qk_norm_rope_backward, m3_linear_attention_forward_workspace, m3_linear_attention_forward,
+    m3_linear_attention_step, m3_linear_attention_backward_workspace,
+    m3_linear_attention_backward)
 from . import inputs  # noqa: F401

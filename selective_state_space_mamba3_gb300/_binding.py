@@ -24,6 +24,8 @@ M3_ERR_TIMEOUT = 5
 M3_ERR_DEVICE_STATE = 6
 M3_MATH_FP32 = 0
 M3_MATH_TF32 = 1
+M3_DTYPE_FP32 = 0
+M3_DTYPE_BF16 = 1
 
 EXPORTED = ("m3_preprocess", "m3_preprocess_backward_workspace", "m3_preprocess_backward",
             "m3_siso_forward_workspace", "m3_siso_forward",
@@ -34,6 +36,10 @@ EXPORTED = ("m3_preprocess", "m3_preprocess_backward_workspace", "m3_preprocess_
             "m3_siso_backward_workspace", "m3_siso_backward",
             "m3_mimo_backward_workspace", "m3_mimo_backward",
             "m3_mimo_forward_workspace", "m3_mimo_forward", "m3_siso_step", "m3_mimo_step",
+            "m3_qk_norm_rope", "m3_qk_norm_rope_backward_workspace", "m3_qk_norm_rope_backward",
+            "m3_linear_attention_forward_workspace", "m3_linear_attention_forward",
+            "m3_linear_attention_step", "m3_linear_attention_backward_workspace",
+            "m3_linear_attention_backward",
             "m3_workspace_status", "m3_selftest_wait_timeout", "m3_status_string",
             "m3_launch_count")
 
@@ -61,6 +67,27 @@ class SsmConfig(ctypes.Structure):
                 ("num_rope_angles", ctypes.c_int64), ("mimo_rank", ctypes.c_int64),
                 ("has_z", ctypes.c_int32), ("has_d", ctypes.c_int32),
                 ("has_output_norm", ctypes.c_int32), ("math_mode", ctypes.c_int32)]
+
+
+class QkNormRopeConfig(ctypes.Structure):
+    """m3_qk_norm_rope_config."""
+    _fields_ = [("rows", ctypes.c_int64), ("num_q_heads", ctypes.c_int64),
+                ("num_k_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("num_rope_angles", ctypes.c_int64), ("max_positions", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64),
+                ("epsilon", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class LinearAttentionConfig(ctypes.Structure):
+    """m3_linear_attention_config."""
+    _fields_ = [("batch_size", ctypes.c_int64), ("sequence_length", ctypes.c_int64),
+                ("total_rows", ctypes.c_int64), ("num_heads", ctypes.c_int64),
+                ("num_groups", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("state_size", ctypes.c_int64), ("num_slots", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 def ssm_config(d: dict, math_mode: int = M3_MATH_FP32) -> SsmConfig:
@@ -119,6 +146,16 @@ def load_library():
         lib.m3_mimo_backward_workspace.argtypes = [cfgp, ctypes.POINTER(ctypes.c_size_t)]
         lib.m3_mimo_backward.argtypes = [cfgp] + [_vp] * 32 + [ctypes.c_size_t, _vp]
         lib.m3_mimo_step.argtypes = [cfgp] + [_vp] * 20 + [_vp]
+        rope, la = ctypes.POINTER(QkNormRopeConfig), ctypes.POINTER(LinearAttentionConfig)
+        szp = ctypes.POINTER(ctypes.c_size_t)
+        lib.m3_qk_norm_rope.argtypes = [rope] + [_vp] * 10
+        lib.m3_qk_norm_rope_backward_workspace.argtypes = [rope, szp]
+        lib.m3_qk_norm_rope_backward.argtypes = [rope] + [_vp] * 14 + [ctypes.c_size_t, _vp]
+        lib.m3_linear_attention_forward_workspace.argtypes = [la, szp]
+        lib.m3_linear_attention_forward.argtypes = [la] + [_vp] * 9 + [ctypes.c_size_t, _vp]
+        lib.m3_linear_attention_step.argtypes = [la] + [_vp] * 8
+        lib.m3_linear_attention_backward_workspace.argtypes = [la, szp]
+        lib.m3_linear_attention_backward.argtypes = [la] + [_vp] * 13 + [ctypes.c_size_t, _vp]
         lib.m3_workspace_status.argtypes = [_vp, ctypes.c_size_t, _vp]
         lib.m3_selftest_wait_timeout.argtypes = [_vp, ctypes.c_size_t, ctypes.c_int64, _vp]
         lib.m3_status_string.argtypes = [ctypes.c_int]
@@ -369,3 +406,197 @@ def m3_selftest_wait_timeout(workspace, budget_cycles, stream=None):
     wp, wn = _ws(workspace)
     _check(load_library().m3_selftest_wait_timeout(wp, wn, int(budget_cycles), _stream(stream)),
            "m3_selftest_wait_timeout")
+
+
+# --- linear-attention operators --------------------------------------------------
+# Activations are CUDA tensors of float32 or bfloat16 shaped [..., heads, width]
+# whose heads are adjacent; the leading dimensions are the rows, any uniform
+# stride apart (views into packed rows are fine).
+
+def _row_stride(t):
+    """Elements from one row of [..., heads, width] to the next."""
+    if t.dim() < 3:
+        raise TypeError("expected a tensor [..., heads, width]")
+    shape, st = t.shape, t.stride()
+    heads, width = shape[-2], shape[-1]
+    if t.numel() == 0:
+        return heads * width
+    if (width > 1 and st[-1] != 1) or (heads > 1 and st[-2] != width):
+        raise TypeError("the heads of a row must be adjacent in memory")
+    step, run = None, 1
+    for size, stride in zip(reversed(shape[:-2]), reversed(st[:-2])):
+        if size > 1:
+            if step is None:
+                step = stride
+            elif stride != step * run:
+                raise TypeError("the rows of an operand must be evenly spaced")
+        run *= size
+    return heads * width if step is None else step
+
+
+def _dtype(t):
+    import torch
+    if t.dtype == torch.float32:
+        return M3_DTYPE_FP32
+    if t.dtype == torch.bfloat16:
+        return M3_DTYPE_BF16
+    raise TypeError("activations must be float32 or bfloat16")
+
+
+def _act(t, cfg, rows, heads, width, stride):
+    """Device pointer of an activation; its shape and stride must be the config's."""
+    if not t.is_cuda or _dtype(t) != cfg.dtype:
+        raise TypeError("activations must be CUDA tensors of the config's type")
+    n = t.numel()
+    if tuple(t.shape[-2:]) != (heads, width) or n != rows * heads * width:
+        raise ValueError(f"expected {rows} rows of [{heads}, {width}], got {tuple(t.shape)}")
+    if _row_stride(t) != (stride or heads * width) and rows > 1:
+        raise ValueError("row stride differs from the config's")
+    return t.data_ptr() if n > 0 else None
+
+
+def _exact(t, dtype_name, shape):
+    """Device pointer of a dense operand of one type and shape (None passes NULL)."""
+    if t is None:
+        return None
+    import torch
+    if not t.is_cuda or t.dtype != getattr(torch, dtype_name) or not t.is_contiguous():
+        raise TypeError(f"expected a contiguous {dtype_name} CUDA tensor")
+    n = 1
+    for x in shape:
+        n *= x
+    if t.numel() != n:
+        raise ValueError(f"expected a tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr() if n > 0 else None
+
+
+def qk_norm_rope_config(q, k, *, num_rope_angles, max_positions=0, epsilon=1e-6, q_out=None,
+                        k_out=None) -> QkNormRopeConfig:
+    """The config of q [..., heads, head_dim] and k (either may be None); outputs
+    are dense unless q_out / k_out say otherwise."""
+    some = q if q is not None else k
+    heads = [0 if t is None else t.shape[-2] for t in (q, k)]
+    strides = [0 if t is None else _row_stride(t) for t in (q, k, q_out, k_out)]
+    width = some.shape[-1]
+    return QkNormRopeConfig(some.numel() // max(1, some.shape[-2] * width), *heads, width,
+                            num_rope_angles, max_positions, *strides, epsilon, _dtype(some))
+
+
+def _rope_operands(cfg, q, k, q_stride, k_stride):
+    out = []
+    for t, heads, stride in ((q, cfg.num_q_heads, q_stride), (k, cfg.num_k_heads, k_stride)):
+        out.append(_act(t, cfg, cfg.rows, heads, cfg.head_dim, stride) if heads else None)
+    return out
+
+
+def _rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions):
+    d, a = cfg.head_dim, cfg.num_rope_angles
+    table = (cfg.max_positions, a) if a else (0,)
+    return [_exact(q_weight, "float32", (d,)), _exact(k_weight, "float32", (d,)),
+            _exact(cos_table, "float32", table), _exact(sin_table, "float32", table),
+            _exact(positions, "int32", (cfg.rows,))]
+
+
+def m3_qk_norm_rope(cfg: QkNormRopeConfig, q, k, q_weight, k_weight, cos_table, sin_table,
+                    positions, q_out, k_out, stream=None):
+    lib = load_library()
+    _check(lib.m3_qk_norm_rope(
+        ctypes.byref(cfg), *_rope_operands(cfg, q, k, cfg.q_stride, cfg.k_stride),
+        *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions),
+        *_rope_operands(cfg, q_out, k_out, cfg.q_out_stride, cfg.k_out_stride), _stream(stream)),
+        "m3_qk_norm_rope")
+
+
+def m3_qk_norm_rope_backward_workspace(cfg: QkNormRopeConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().m3_qk_norm_rope_backward_workspace(ctypes.byref(cfg), ctypes.byref(n)),
+           "m3_qk_norm_rope_backward_workspace")
+    return n.value
+
+
+def m3_qk_norm_rope_backward(cfg: QkNormRopeConfig, q, k, q_weight, k_weight, cos_table, sin_table,
+                             positions, grad_q_out, grad_k_out, grad_q, grad_k, grad_q_weight,
+                             grad_k_weight, workspace=None, stream=None):
+    wp, wn = _ws(workspace)
+    d = (cfg.head_dim,)
+    _check(load_library().m3_qk_norm_rope_backward(
+        ctypes.byref(cfg), *_rope_operands(cfg, q, k, cfg.q_stride, cfg.k_stride),
+        *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions),
+        *_rope_operands(cfg, grad_q_out, grad_k_out, cfg.q_out_stride, cfg.k_out_stride),
+        *_rope_operands(cfg, grad_q, grad_k, 0, 0), _exact(grad_q_weight, "float32", d),
+        _exact(grad_k_weight, "float32", d), wp, wn, _stream(stream)), "m3_qk_norm_rope_backward")
+
+
+def linear_attention_config(q, k, v, *, batch_size, sequence_length, num_heads=None, num_groups=0,
+                            scale=1.0, num_slots=0, out=None) -> LinearAttentionConfig:
+    """The config of q, k [..., groups, state_size] and v [..., heads, head_dim];
+    out is dense unless given."""
+    heads = v.shape[-2] if num_heads is None else num_heads
+    strides = [0 if t is None else _row_stride(t) for t in (q, k, v, out)]
+    return LinearAttentionConfig(batch_size, sequence_length,
+                                 v.numel() // max(1, v.shape[-2] * v.shape[-1]), heads, num_groups,
+                                 v.shape[-1], q.shape[-1], num_slots, *strides, scale, _dtype(v))
+
+
+def _la_qkv(cfg, q, k, v):
+    r, g = cfg.total_rows, cfg.num_groups or cfg.num_heads
+    return [_act(q, cfg, r, g, cfg.state_size, cfg.q_stride),
+            _act(k, cfg, r, g, cfg.state_size, cfg.k_stride),
+            _act(v, cfg, r, cfg.num_heads, cfg.head_dim, cfg.v_stride)]
+
+
+def _la_state(cfg, t, count):
+    return _exact(t, "float32", (count, cfg.num_heads, cfg.head_dim, cfg.state_size))
+
+
+def _la_out(cfg, t):
+    return _act(t, cfg, cfg.total_rows, cfg.num_heads, cfg.head_dim, cfg.out_stride)
+
+
+def m3_linear_attention_forward_workspace(cfg: LinearAttentionConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().m3_linear_attention_forward_workspace(ctypes.byref(cfg), ctypes.byref(n)),
+           "m3_linear_attention_forward_workspace")
+    return n.value
+
+
+def m3_linear_attention_forward(cfg: LinearAttentionConfig, q, k, v, log_decay, offsets,
+                                initial_state, out, final_state, workspace=None, stream=None):
+    wp, wn = _ws(workspace)
+    b = cfg.batch_size
+    _check(load_library().m3_linear_attention_forward(
+        ctypes.byref(cfg), *_la_qkv(cfg, q, k, v), _exact(log_decay, "float32", (cfg.num_heads,)),
+        _exact(offsets, "int32", (b + 1,)), _la_state(cfg, initial_state, b), _la_out(cfg, out),
+        _la_state(cfg, final_state, b), wp, wn, _stream(stream)), "m3_linear_attention_forward")
+
+
+def m3_linear_attention_step(cfg: LinearAttentionConfig, q, k, v, log_decay, slots, state, out,
+                             stream=None):
+    count = cfg.num_slots or cfg.batch_size
+    _check(load_library().m3_linear_attention_step(
+        ctypes.byref(cfg), *_la_qkv(cfg, q, k, v), _exact(log_decay, "float32", (cfg.num_heads,)),
+        _exact(slots, "int32", (cfg.batch_size,)), _la_state(cfg, state, count), _la_out(cfg, out),
+        _stream(stream)), "m3_linear_attention_step")
+
+
+def m3_linear_attention_backward_workspace(cfg: LinearAttentionConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().m3_linear_attention_backward_workspace(ctypes.byref(cfg),
+                                                                 ctypes.byref(n)),
+           "m3_linear_attention_backward_workspace")
+    return n.value
+
+
+def m3_linear_attention_backward(cfg: LinearAttentionConfig, grad_out, q, k, v, log_decay, offsets,
+                                 initial_state, grad_final_state, grad_q, grad_k, grad_v,
+                                 grad_initial_state, workspace=None, stream=None):
+    wp, wn = _ws(workspace)
+    b, r, h = cfg.batch_size, cfg.total_rows, cfg.num_heads
+    g = cfg.num_groups or h
+    _check(load_library().m3_linear_attention_backward(
+        ctypes.byref(cfg), _la_out(cfg, grad_out), *_la_qkv(cfg, q, k, v),
+        _exact(log_decay, "float32", (h,)), _exact(offsets, "int32", (b + 1,)),
+        _la_state(cfg, initial_state, b), _la_state(cfg, grad_final_state, b),
+        _act(grad_q, cfg, r, g, cfg.state_size, 0), _act(grad_k, cfg, r, g, cfg.state_size, 0),
+        _act(grad_v, cfg, r, h, cfg.head_dim, 0), _la_state(cfg, grad_initial_state, b), wp, wn,
+        _stream(stream)), "m3_linear_attention_backward")

@@ -1,0 +1,130 @@
+// Internal declarations of the linear-attention operators (m3_qk_norm_rope,
+// m3_linear_attention_*). Validation and dispatch: m3_linattn.cu. Kernels:
+// k_qk_norm_rope.cu, k_linattn_seq.cu (prompts and adjoints, any shape),
+// k_linattn_step.cu.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "m3_internal.cuh"
+
+namespace m3 {
+
+// --- norm and rotation of queries and keys ---------------------------------
+struct RopeSide {
+  const void *x, *dy;  // input; output gradient (backward)
+  void* y;             // output, or input gradient
+  const float* w;      // null: ones
+  int64_t xs, ys, dys; // row strides in elements
+  int heads;
+};
+struct RopeArgs {
+  RopeSide side[2];  // queries, keys
+  const float *cos_table, *sin_table;
+  const int32_t* positions;
+  float* gw[2];      // weight gradients (backward; may be null)
+  float* partial;    // backward: per-block weight sums
+  int64_t rows;
+  int D, A, max_pos, dtype;
+  float eps;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t s);
+size_t qk_norm_rope_backward_bytes(const RopeArgs& a);
+cudaError_t launch_qk_norm_rope_backward(const RopeArgs& a, cudaStream_t s);
+
+// --- linear attention --------------------------------------------------------
+// One recurrence over the tokens of every sequence and head,
+//   out_t = intra * sum_u lam^|t-u| (q_t.k_u) v_u + inter * lam^(...) state q_t,
+//   state' = lam^n state + kv * sum_u lam^(...) v_u k_u^T,
+// u <= t walking up, or u >= t walking down (reverse). The forward pass is one
+// of them; the backward pass is three, with the operands' roles exchanged.
+// N is the width of q and k here, P that of v and out.
+struct LaRole {
+  const void *q, *k, *v;
+  void* out;
+  int64_t qs, ks, vs, os;     // row strides in elements
+  int q_rep, k_rep, v_rep;    // heads that share one head of the operand
+  int out_rep;                // 1, or: out is float32 [rows, H, P] partials to be summed over so many heads
+  int N, P;
+  int reverse;
+  float intra, inter, kv;
+  const float* init;          // entry state per (b, h), element (p, n) at p * sp + n * sn
+  float* fin;                 // final state, same layout (null: not wanted)
+  int sp, sn;
+  int shift;                  // the entry state counts as of this many tokens later (0 or 1)
+  int fin_shift;              // decays applied to the final state of a non-empty sequence (0 or 1)
+};
+
+constexpr int kLaChunk = 128;  // segments are whole numbers of this many tokens
+
+struct LaArgs {
+  LaRole role[3];
+  int nrole;
+  int B, H, dtype;
+  int64_t L, rows;
+  const float* log_decay;
+  const int32_t* offsets;
+  // long sequences are cut into nseg segments of seg_len tokens: `entry` has,
+  // for each (role, segment, b, h), first the segment's own state sum
+  // (summary pass), then its entry state (prefix pass); states as [P][N]
+  int nseg;
+  int64_t seg_len;
+  float* entry;
+  int64_t entry_role;  // floats per role in `entry`
+  uint32_t* status;
+};
+
+enum LaPass { kLaMain = 0, kLaSummary = 1 };
+cudaError_t launch_la_seq(const LaArgs& a, LaPass pass, cudaStream_t s);
+cudaError_t launch_la_prefix(const LaArgs& a, cudaStream_t s);
+// out[row][g][w] = sum over the group's heads of part[row][h][w], in head order
+cudaError_t launch_la_group_sum(const LaArgs& a, const float* part, void* out, int groups, int rep,
+                                int width, cudaStream_t s);
+
+struct LaStepArgs {
+  const void *q, *k, *v;
+  void* out;
+  float* state;
+  const float* log_decay;
+  const int32_t* slots;
+  int64_t qs, ks, vs, os;
+  int B, H, rep, P, N, dtype;
+  int64_t num_slots;
+  float scale;
+};
+cudaError_t launch_la_step(const LaStepArgs& a, cudaStream_t s);
+
+// --- shared device helpers ---------------------------------------------------
+template <typename T>
+__device__ __forceinline__ float to_f32(T v) {
+  return (float)v;
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float v) {
+  return (T)v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
+  return __float2bfloat16_rn(v);
+}
+
+// Rows [begin, end) of sequence b; offsets outside [0, rows] count as the
+// nearest row inside, and a sequence is at most L rows long.
+__device__ __forceinline__ void la_rows(const LaArgs& a, int b, int64_t* begin, int64_t* len) {
+  if (!a.offsets) {
+    *begin = (int64_t)b * a.L;
+    *len = a.L;
+    return;
+  }
+  const int64_t lo = min(max((int64_t)a.offsets[b], (int64_t)0), a.rows);
+  const int64_t hi = min(max((int64_t)a.offsets[b + 1], lo), a.rows);
+  *begin = lo;
+  *len = min(hi - lo, a.L);
+}
+
+// lam^d for d >= 0 (lam = e^ld; 0 * -inf counts as 0).
+__device__ __forceinline__ float la_power(float ld, int64_t d) {
+  return d == 0 ? 1.0f : expf(ld * (float)d);
+}
+
+}  // namespace m3
