@@ -1,7 +1,7 @@
 // Internal declarations of the linear-attention operators (m3_qk_norm_rope,
 // m3_linear_attention_*). Validation and dispatch: m3_linattn.cu. Kernels:
-// k_qk_norm_rope.cu, k_linattn_seq.cu (prompts and adjoints, any shape),
-// k_linattn_step.cu.
+// k_qk_norm_rope.cu, k_linattn_mma.cu (prompts and adjoints on the tensor cores),
+// k_linattn_seq.cu (the same, any shape), k_linattn_step.cu.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -76,6 +76,10 @@ struct LaArgs {
 
 enum LaPass { kLaMain = 0, kLaSummary = 1 };
 cudaError_t launch_la_seq(const LaArgs& a, LaPass pass, cudaStream_t s);
+// bfloat16 operands that tile copies take (widths and strides multiples of
+// eight elements, 16-byte addresses): the tensor-core kernel
+bool la_mma_supported(const LaArgs& a);
+cudaError_t launch_la_mma(const LaArgs& a, LaPass pass, cudaStream_t s);
 cudaError_t launch_la_prefix(const LaArgs& a, cudaStream_t s);
 // out[row][g][w] = sum over the group's heads of part[row][h][w], in head order
 cudaError_t launch_la_group_sum(const LaArgs& a, const float* part, void* out, int groups, int rep,

@@ -8,7 +8,7 @@ namespace m3 {
 namespace {
 
 constexpr int64_t kMaxRows = (int64_t)1 << 31;  // row numbers are 32-bit in offsets and tile copies
-constexpr int64_t kMaxStride = (int64_t)1 << 40;
+constexpr int64_t kMaxStride = (int64_t)1 << 38;  // elements; tile copies take byte strides below 2^40
 
 bool aligned_to(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? M3_OK : M3_ERR_CUDA; }
@@ -123,10 +123,14 @@ int check_rows(const La& g, const int32_t* offsets) {
   return g.rows == (int64_t)g.B * g.L ? M3_OK : M3_ERR_INVALID_ARGUMENT;
 }
 
-// Sequences shorter of blocks than the SMs take (two a SM) are cut into
-// segments of at least four chunks.
-void choose_segments(const La& g, int nrole, int* nseg, int64_t* seg_len) {
-  const int64_t blocks = (int64_t)g.B * g.H * nrole, chunks = (g.L + kLaChunk - 1) / kLaChunk;
+// Calls with fewer blocks than the SMs take (two an SM) cut their sequences
+// into segments of at least four chunks. The tensor-core kernel has a block for
+// every 64 output columns, the other one for every head.
+void choose_segments(const La& g, bool backward, int* nseg, int64_t* seg_len) {
+  const int tp = g.dtype == M3_DTYPE_BF16 ? (g.P + 63) / 64 : 1;
+  const int tn = g.dtype == M3_DTYPE_BF16 ? (g.N + 63) / 64 : 1;
+  const int64_t blocks = (int64_t)g.B * g.H * (backward ? 2 * tn + tp : tp);
+  const int64_t chunks = (g.L + kLaChunk - 1) / kLaChunk;
   int64_t n = 304 / blocks;
   if (n > chunks / 4) n = chunks / 4;
   if (n < 1) n = 1;
@@ -148,7 +152,7 @@ struct LaWork {
 LaWork la_work(const La& g, bool backward) {
   LaWork w{};
   const int nrole = backward ? 3 : 1;
-  choose_segments(g, nrole, &w.nseg, &w.seg_len);
+  choose_segments(g, backward, &w.nseg, &w.seg_len);
   size_t o = kStatusBytes;
   w.entry = o;
   if (w.nseg > 1) o += round256((size_t)nrole * w.nseg * g.B * g.H * g.N * g.P * 4);
@@ -179,11 +183,12 @@ LaArgs base_args(const La& g, const LaWork& w, int nrole, const float* ld, const
 int run_la(const LaArgs& a, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(a.status, 0, 16, s);
   if (e != cudaSuccess) return M3_ERR_CUDA;
+  auto* const launch = la_mma_supported(a) ? launch_la_mma : launch_la_seq;
   if (a.nseg > 1) {
-    if ((e = launch_la_seq(a, kLaSummary, s)) != cudaSuccess) return M3_ERR_CUDA;
+    if ((e = launch(a, kLaSummary, s)) != cudaSuccess) return M3_ERR_CUDA;
     if ((e = launch_la_prefix(a, s)) != cudaSuccess) return M3_ERR_CUDA;
   }
-  return cuda_status(launch_la_seq(a, kLaMain, s));
+  return cuda_status(launch(a, kLaMain, s));
 }
 
 int check_workspace(const void* ws, size_t bytes, size_t want) {
