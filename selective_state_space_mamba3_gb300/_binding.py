@@ -111,6 +111,8 @@ _vp = ctypes.c_void_p
 def load_library():
     """Loads libm3.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -411,7 +413,30 @@ def m3_selftest_wait_timeout(workspace, budget_cycles, stream=None):
 # --- linear-attention operators --------------------------------------------------
 # Activations are CUDA tensors of float32 or bfloat16 shaped [..., heads, width]
 # whose heads are adjacent; the leading dimensions are the rows, any uniform
-# stride apart (views into packed rows are fine).
+# stride apart (views into packed rows are fine). The calls for single tokens
+# take a few microseconds on the GPU, so every check has a short form for the
+# tensor that is as expected: no import, no attribute twice.
+
+_types = None
+
+
+def _torch_types():
+    """(float32, bfloat16, int32, the raw handle of a device's current stream)."""
+    global _types
+    if _types is None:
+        import torch
+        _types = (torch.float32, torch.bfloat16, torch.int32,
+                  getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                  (lambda i: torch.cuda.current_stream(i).cuda_stream))
+    return _types
+
+
+def _stream_of(stream, t):
+    """The given stream, or the current one of the device that holds t."""
+    if stream is not None:
+        return stream if isinstance(stream, int) else stream.cuda_stream
+    return _torch_types()[3](t.device.index)
+
 
 def _row_stride(t):
     """Elements from one row of [..., heads, width] to the next."""
@@ -435,39 +460,45 @@ def _row_stride(t):
 
 
 def _dtype(t):
-    import torch
-    if t.dtype == torch.float32:
+    types = _torch_types()
+    if t.dtype == types[0]:
         return M3_DTYPE_FP32
-    if t.dtype == torch.bfloat16:
+    if t.dtype == types[1]:
         return M3_DTYPE_BF16
     raise TypeError("activations must be float32 or bfloat16")
 
 
-def _act(t, cfg, rows, heads, width, stride):
+def _act(t, dtype, rows, heads, width, stride):
     """Device pointer of an activation; its shape and stride must be the config's."""
-    if not t.is_cuda or _dtype(t) != cfg.dtype:
+    stride = stride or heads * width
+    if (t.dtype is dtype and t.is_cuda and rows and t.shape == (rows, heads, width) and
+            t.stride() == (stride, width, 1)):
+        return t.data_ptr()
+    if not t.is_cuda or t.dtype != dtype:
         raise TypeError("activations must be CUDA tensors of the config's type")
     n = t.numel()
     if tuple(t.shape[-2:]) != (heads, width) or n != rows * heads * width:
         raise ValueError(f"expected {rows} rows of [{heads}, {width}], got {tuple(t.shape)}")
-    if _row_stride(t) != (stride or heads * width) and rows > 1:
+    if _row_stride(t) != stride and rows > 1:
         raise ValueError("row stride differs from the config's")
     return t.data_ptr() if n > 0 else None
 
 
-def _exact(t, dtype_name, shape):
+def _dense(t, dtype, shape):
     """Device pointer of a dense operand of one type and shape (None passes NULL)."""
     if t is None:
         return None
-    import torch
-    if not t.is_cuda or t.dtype != getattr(torch, dtype_name) or not t.is_contiguous():
-        raise TypeError(f"expected a contiguous {dtype_name} CUDA tensor")
-    n = 1
-    for x in shape:
-        n *= x
-    if t.numel() != n:
-        raise ValueError(f"expected a tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr() if n > 0 else None
+    if not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+        raise TypeError(f"expected a contiguous {dtype} CUDA tensor")
+    if t.shape != shape:
+        n = 1
+        for x in shape:
+            n *= x
+        if t.numel() != n:
+            raise ValueError(f"expected a tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+        if n == 0:
+            return None
+    return t.data_ptr()
 
 
 def qk_norm_rope_config(q, k, *, num_rope_angles, max_positions=0, epsilon=1e-6, q_out=None,
@@ -482,29 +513,29 @@ def qk_norm_rope_config(q, k, *, num_rope_angles, max_positions=0, epsilon=1e-6,
                             num_rope_angles, max_positions, *strides, epsilon, _dtype(some))
 
 
-def _rope_operands(cfg, q, k, q_stride, k_stride):
-    out = []
-    for t, heads, stride in ((q, cfg.num_q_heads, q_stride), (k, cfg.num_k_heads, k_stride)):
-        out.append(_act(t, cfg, cfg.rows, heads, cfg.head_dim, stride) if heads else None)
-    return out
+def _rope_operands(cfg, dtype, q, k, q_stride, k_stride):
+    rows, d, hq, hk = cfg.rows, cfg.head_dim, cfg.num_q_heads, cfg.num_k_heads
+    return (_act(q, dtype, rows, hq, d, q_stride) if hq else None,
+            _act(k, dtype, rows, hk, d, k_stride) if hk else None)
 
 
 def _rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions):
-    d, a = cfg.head_dim, cfg.num_rope_angles
+    f32, _, i32, _ = _torch_types()
+    d, a = (cfg.head_dim,), cfg.num_rope_angles
     table = (cfg.max_positions, a) if a else (0,)
-    return [_exact(q_weight, "float32", (d,)), _exact(k_weight, "float32", (d,)),
-            _exact(cos_table, "float32", table), _exact(sin_table, "float32", table),
-            _exact(positions, "int32", (cfg.rows,))]
+    return (_dense(q_weight, f32, d), _dense(k_weight, f32, d), _dense(cos_table, f32, table),
+            _dense(sin_table, f32, table), _dense(positions, i32, (cfg.rows,)))
 
 
 def m3_qk_norm_rope(cfg: QkNormRopeConfig, q, k, q_weight, k_weight, cos_table, sin_table,
                     positions, q_out, k_out, stream=None):
     lib = load_library()
+    dt = _torch_types()[cfg.dtype]
     _check(lib.m3_qk_norm_rope(
-        ctypes.byref(cfg), *_rope_operands(cfg, q, k, cfg.q_stride, cfg.k_stride),
+        ctypes.byref(cfg), *_rope_operands(cfg, dt, q, k, cfg.q_stride, cfg.k_stride),
         *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions),
-        *_rope_operands(cfg, q_out, k_out, cfg.q_out_stride, cfg.k_out_stride), _stream(stream)),
-        "m3_qk_norm_rope")
+        *_rope_operands(cfg, dt, q_out, k_out, cfg.q_out_stride, cfg.k_out_stride),
+        _stream_of(stream, k if q is None else q)), "m3_qk_norm_rope")
 
 
 def m3_qk_norm_rope_backward_workspace(cfg: QkNormRopeConfig) -> int:
@@ -518,13 +549,15 @@ def m3_qk_norm_rope_backward(cfg: QkNormRopeConfig, q, k, q_weight, k_weight, co
                              positions, grad_q_out, grad_k_out, grad_q, grad_k, grad_q_weight,
                              grad_k_weight, workspace=None, stream=None):
     wp, wn = _ws(workspace)
-    d = (cfg.head_dim,)
+    types = _torch_types()
+    d, dt = (cfg.head_dim,), types[cfg.dtype]
     _check(load_library().m3_qk_norm_rope_backward(
-        ctypes.byref(cfg), *_rope_operands(cfg, q, k, cfg.q_stride, cfg.k_stride),
+        ctypes.byref(cfg), *_rope_operands(cfg, dt, q, k, cfg.q_stride, cfg.k_stride),
         *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions),
-        *_rope_operands(cfg, grad_q_out, grad_k_out, cfg.q_out_stride, cfg.k_out_stride),
-        *_rope_operands(cfg, grad_q, grad_k, 0, 0), _exact(grad_q_weight, "float32", d),
-        _exact(grad_k_weight, "float32", d), wp, wn, _stream(stream)), "m3_qk_norm_rope_backward")
+        *_rope_operands(cfg, dt, grad_q_out, grad_k_out, cfg.q_out_stride, cfg.k_out_stride),
+        *_rope_operands(cfg, dt, grad_q, grad_k, 0, 0), _dense(grad_q_weight, types[0], d),
+        _dense(grad_k_weight, types[0], d), wp, wn, _stream_of(stream, k if q is None else q)),
+        "m3_qk_norm_rope_backward")
 
 
 def linear_attention_config(q, k, v, *, batch_size, sequence_length, num_heads=None, num_groups=0,
@@ -538,19 +571,27 @@ def linear_attention_config(q, k, v, *, batch_size, sequence_length, num_heads=N
                                  v.shape[-1], q.shape[-1], num_slots, *strides, scale, _dtype(v))
 
 
-def _la_qkv(cfg, q, k, v):
-    r, g = cfg.total_rows, cfg.num_groups or cfg.num_heads
-    return [_act(q, cfg, r, g, cfg.state_size, cfg.q_stride),
-            _act(k, cfg, r, g, cfg.state_size, cfg.k_stride),
-            _act(v, cfg, r, cfg.num_heads, cfg.head_dim, cfg.v_stride)]
+class _LaShapes:
+    """Checks of one call's operands against its config."""
+    __slots__ = ("dt", "f32", "i32", "b", "r", "h", "g", "n", "p")
 
+    def __init__(self, cfg):
+        types = _torch_types()
+        self.f32, self.i32, self.dt = types[0], types[2], types[cfg.dtype]
+        self.b, self.r, self.h = cfg.batch_size, cfg.total_rows, cfg.num_heads
+        self.g, self.n, self.p = cfg.num_groups or self.h, cfg.state_size, cfg.head_dim
 
-def _la_state(cfg, t, count):
-    return _exact(t, "float32", (count, cfg.num_heads, cfg.head_dim, cfg.state_size))
+    def qk(self, t, stride):
+        return _act(t, self.dt, self.r, self.g, self.n, stride)
 
+    def vo(self, t, stride):
+        return _act(t, self.dt, self.r, self.h, self.p, stride)
 
-def _la_out(cfg, t):
-    return _act(t, cfg, cfg.total_rows, cfg.num_heads, cfg.head_dim, cfg.out_stride)
+    def state(self, t, count):
+        return _dense(t, self.f32, (count, self.h, self.p, self.n))
+
+    def decay(self, t):
+        return _dense(t, self.f32, (self.h,))
 
 
 def m3_linear_attention_forward_workspace(cfg: LinearAttentionConfig) -> int:
@@ -563,20 +604,21 @@ def m3_linear_attention_forward_workspace(cfg: LinearAttentionConfig) -> int:
 def m3_linear_attention_forward(cfg: LinearAttentionConfig, q, k, v, log_decay, offsets,
                                 initial_state, out, final_state, workspace=None, stream=None):
     wp, wn = _ws(workspace)
-    b = cfg.batch_size
+    x = _LaShapes(cfg)
     _check(load_library().m3_linear_attention_forward(
-        ctypes.byref(cfg), *_la_qkv(cfg, q, k, v), _exact(log_decay, "float32", (cfg.num_heads,)),
-        _exact(offsets, "int32", (b + 1,)), _la_state(cfg, initial_state, b), _la_out(cfg, out),
-        _la_state(cfg, final_state, b), wp, wn, _stream(stream)), "m3_linear_attention_forward")
+        ctypes.byref(cfg), x.qk(q, cfg.q_stride), x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride),
+        x.decay(log_decay), _dense(offsets, x.i32, (x.b + 1,)), x.state(initial_state, x.b),
+        x.vo(out, cfg.out_stride), x.state(final_state, x.b), wp, wn, _stream_of(stream, v)),
+        "m3_linear_attention_forward")
 
 
 def m3_linear_attention_step(cfg: LinearAttentionConfig, q, k, v, log_decay, slots, state, out,
                              stream=None):
-    count = cfg.num_slots or cfg.batch_size
+    x = _LaShapes(cfg)
     _check(load_library().m3_linear_attention_step(
-        ctypes.byref(cfg), *_la_qkv(cfg, q, k, v), _exact(log_decay, "float32", (cfg.num_heads,)),
-        _exact(slots, "int32", (cfg.batch_size,)), _la_state(cfg, state, count), _la_out(cfg, out),
-        _stream(stream)), "m3_linear_attention_step")
+        ctypes.byref(cfg), x.qk(q, cfg.q_stride), x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride),
+        x.decay(log_decay), _dense(slots, x.i32, (x.b,)), x.state(state, cfg.num_slots or x.b),
+        x.vo(out, cfg.out_stride), _stream_of(stream, v)), "m3_linear_attention_step")
 
 
 def m3_linear_attention_backward_workspace(cfg: LinearAttentionConfig) -> int:
@@ -591,12 +633,11 @@ def m3_linear_attention_backward(cfg: LinearAttentionConfig, grad_out, q, k, v, 
                                  initial_state, grad_final_state, grad_q, grad_k, grad_v,
                                  grad_initial_state, workspace=None, stream=None):
     wp, wn = _ws(workspace)
-    b, r, h = cfg.batch_size, cfg.total_rows, cfg.num_heads
-    g = cfg.num_groups or h
+    x = _LaShapes(cfg)
     _check(load_library().m3_linear_attention_backward(
-        ctypes.byref(cfg), _la_out(cfg, grad_out), *_la_qkv(cfg, q, k, v),
-        _exact(log_decay, "float32", (h,)), _exact(offsets, "int32", (b + 1,)),
-        _la_state(cfg, initial_state, b), _la_state(cfg, grad_final_state, b),
-        _act(grad_q, cfg, r, g, cfg.state_size, 0), _act(grad_k, cfg, r, g, cfg.state_size, 0),
-        _act(grad_v, cfg, r, h, cfg.head_dim, 0), _la_state(cfg, grad_initial_state, b), wp, wn,
-        _stream(stream)), "m3_linear_attention_backward")
+        ctypes.byref(cfg), x.vo(grad_out, cfg.out_stride), x.qk(q, cfg.q_stride),
+        x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride), x.decay(log_decay),
+        _dense(offsets, x.i32, (x.b + 1,)), x.state(initial_state, x.b),
+        x.state(grad_final_state, x.b), x.qk(grad_q, 0), x.qk(grad_k, 0), x.vo(grad_v, 0),
+        x.state(grad_initial_state, x.b), wp, wn, _stream_of(stream, v)),
+        "m3_linear_attention_backward")

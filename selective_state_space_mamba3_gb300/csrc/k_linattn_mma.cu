@@ -34,8 +34,7 @@
 #include <cudaTypedefs.h>
 #include <string.h>
 
-#include "linattn.cuh"
-#include "tc_ptx.cuh"
+#include "linattn_mma.cuh"
 
 namespace m3 {
 namespace {
@@ -64,22 +63,6 @@ struct Maps {
   CUtensorMap q[3], k[3], v[3], out[3];
 };
 
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc));
-}
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc));
-}
 // K-major 128-byte-swizzled operand: 8-row groups 1024 B apart; 16 columns on = 32 B,
 // 64 columns on = one block.
 __device__ __forceinline__ uint64_t kmajor(uint32_t addr, int ks) {
@@ -114,39 +97,6 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* m, uint32_t src, in
 __device__ __forceinline__ void tma_store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
-__device__ __forceinline__ void pair_sync(int id) {
-  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
-}
-// 16 columns of this warp's 32 lanes, no wait.
-__device__ __forceinline__ void ld16(uint32_t addr, float* v) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(addr));
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-// Byte offset of the 16-byte chunk `c` of row r in a swizzled block.
-__device__ __forceinline__ uint32_t chunk_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-__device__ __forceinline__ uint4 lds(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void sts(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
-
 // One block's walk. NB: 64-column blocks of N (1: N <= 64, 2: N <= 128).
 template <int NB, bool SUMMARY>
 __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, int pt, int bh,
@@ -492,6 +442,7 @@ template <bool SUMMARY>
 __global__ void __launch_bounds__(kThreads, 2)
     k_la_mma(const __grid_constant__ LaArgs a, const __grid_constant__ Maps maps, int items) {
   extern __shared__ __align__(1024) char raw[];
+  la_clear_status<SUMMARY>(a);
   int item = blockIdx.x % items, ri = 0;
   const int unit = blockIdx.x / items;
   while (item >= (a.role[ri].P + 63) / 64) item -= (a.role[ri++].P + 63) / 64;

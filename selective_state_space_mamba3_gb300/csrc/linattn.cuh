@@ -1,7 +1,8 @@
 // Internal declarations of the linear-attention operators (m3_qk_norm_rope,
 // m3_linear_attention_*). Validation and dispatch: m3_linattn.cu. Kernels:
-// k_qk_norm_rope.cu, k_linattn_mma.cu (prompts and adjoints on the tensor cores),
-// k_linattn_seq.cu (the same, any shape), k_linattn_step.cu.
+// k_qk_norm_rope.cu, k_linattn_mma.cu (prompts and adjoints, bfloat16),
+// k_linattn_split.cu (float32, and any width or alignment), k_linattn_state.cu
+// (states of segments, sums over shared heads), k_linattn_step.cu.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -75,7 +76,8 @@ struct LaArgs {
 };
 
 enum LaPass { kLaMain = 0, kLaSummary = 1 };
-cudaError_t launch_la_seq(const LaArgs& a, LaPass pass, cudaStream_t s);
+// float32 activations, and bfloat16 ones that the other kernel does not take
+cudaError_t launch_la_split(const LaArgs& a, LaPass pass, cudaStream_t s);
 // bfloat16 operands that tile copies take (widths and strides multiples of
 // eight elements, 16-byte addresses): the tensor-core kernel
 bool la_mma_supported(const LaArgs& a);
@@ -124,6 +126,13 @@ __device__ __forceinline__ void la_rows(const LaArgs& a, int b, int64_t* begin, 
   const int64_t hi = min(max((int64_t)a.offsets[b + 1], lo), a.rows);
   *begin = lo;
   *len = min(hi - lo, a.L);
+}
+
+// The call's first kernel clears the status word; a wait gives up only after
+// about two seconds.
+template <bool SUMMARY>
+__device__ __forceinline__ void la_clear_status(const LaArgs& a) {
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (SUMMARY || a.nseg == 1)) atomicExch(a.status, 0u);
 }
 
 // lam^d for d >= 0 (lam = e^ld; 0 * -inf counts as 0).

@@ -123,20 +123,27 @@ int check_rows(const La& g, const int32_t* offsets) {
   return g.rows == (int64_t)g.B * g.L ? M3_OK : M3_ERR_INVALID_ARGUMENT;
 }
 
-// Calls with fewer blocks than the SMs take (two an SM) cut their sequences
-// into segments of at least four chunks. The tensor-core kernel has a block for
-// every 64 output columns, the other one for every head.
+// Segments a sequence is cut into, of at least four chunks: the number with the
+// shortest pass, in chunks walked one after another. The kernels have a block
+// for every 64 output columns, and the SMs hold two (bfloat16) or one (float32)
+// each. A cut call walks every segment twice, the first time (states alone) in
+// about half the time, and starts two more kernels, about two chunks' time.
 void choose_segments(const La& g, bool backward, int* nseg, int64_t* seg_len) {
-  const int tp = g.dtype == M3_DTYPE_BF16 ? (g.P + 63) / 64 : 1;
-  const int tn = g.dtype == M3_DTYPE_BF16 ? (g.N + 63) / 64 : 1;
+  const int tp = (g.P + 63) / 64, tn = (g.N + 63) / 64;
   const int64_t blocks = (int64_t)g.B * g.H * (backward ? 2 * tn + tp : tp);
+  const int64_t slots = g.dtype == M3_DTYPE_BF16 ? 304 : 152;
   const int64_t chunks = (g.L + kLaChunk - 1) / kLaChunk;
-  int64_t n = 304 / blocks;
-  if (n > chunks / 4) n = chunks / 4;
-  if (n < 1) n = 1;
-  const int64_t per = (chunks + n - 1) / n;
-  *nseg = (int)((chunks + per - 1) / per);
-  *seg_len = per * kLaChunk;
+  double best = 0;
+  for (int64_t n = 1; n == 1 || (n <= 64 && n <= chunks / 4); ++n) {
+    const int64_t per = (chunks + n - 1) / n, segs = (chunks + per - 1) / per;
+    const double turns = (double)((blocks * segs + slots - 1) / slots) * per;
+    const double cost = segs > 1 ? 1.5 * turns + 2 : turns;
+    if (n == 1 || cost < best) {
+      best = cost;
+      *nseg = (int)segs;
+      *seg_len = per * kLaChunk;
+    }
+  }
 }
 
 constexpr size_t kStatusBytes = 256;
@@ -181,9 +188,8 @@ LaArgs base_args(const La& g, const LaWork& w, int nrole, const float* ld, const
 }
 
 int run_la(const LaArgs& a, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(a.status, 0, 16, s);
-  if (e != cudaSuccess) return M3_ERR_CUDA;
-  auto* const launch = la_mma_supported(a) ? launch_la_mma : launch_la_seq;
+  cudaError_t e;
+  auto* const launch = la_mma_supported(a) ? launch_la_mma : launch_la_split;
   if (a.nseg > 1) {
     if ((e = launch(a, kLaSummary, s)) != cudaSuccess) return M3_ERR_CUDA;
     if ((e = launch_la_prefix(a, s)) != cudaSuccess) return M3_ERR_CUDA;
