@@ -69,26 +69,10 @@ __device__ __forceinline__ void sts2(uint32_t a, uint32_t x, uint32_t y) {
 __device__ __forceinline__ uint32_t quad_at(int r, int c) {
   return (c >> 6) * kBlk + chunk_at(r, (c & 63) >> 3) + ((c & 4) << 1);
 }
-__device__ __forceinline__ uint64_t kmajor(uint32_t addr, int ks) {
-  return tc::sdesc(addr + (ks >> 2) * kBlk + (ks & 3) * 32, 16, 1024) | (2ull << 61);
-}
-__device__ __forceinline__ uint64_t mnmajor(uint32_t addr, int ks) {
-  return tc::sdesc(addr + ks * 2048, kBlk, 1024) | (2ull << 61);
-}
-__device__ __forceinline__ void st8(uint32_t addr, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
-               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-__device__ __forceinline__ void ld_m64_8(uint32_t addr, float* v) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(addr));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
+__device__ __forceinline__ uint32_t kmajor(uint32_t addr) { return (uint32_t)tc::sdesc(addr, 16, 1024); }
+__device__ __forceinline__ uint32_t mnmajor(uint32_t addr) { return (uint32_t)tc::sdesc(addr, kBlk, 1024); }
+__host__ __device__ constexpr uint32_t kstep(int ks) { return ((ks >> 2) * kBlk + (ks & 3) * 32) >> 4; }
+__host__ __device__ constexpr uint32_t mnstep(int ks) { return ks * 2048 >> 4; }
 // Four values of a row of `width`, zeros past it.
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p, int c, int width, bool vec);
@@ -318,12 +302,12 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
         const int ksq = (N + 15) / 16;
         products(IP, IP, [&](int i, int j, bool acc) {
           for (int ks = 0; ks < ksq; ++ks)
-            mma_ts(tm + kColA, tm + kColQ + 64 * i + 8 * ks, kmajor(sK + j * kPartK, ks),
+            mma_ts(tm + kColA, tm + kColQ + 64 * i, 8 * ks, kmajor(sK + j * kPartK), kstep(ks),
                    idesc_bf16(128, kC, 0, 0), acc || ks > 0);
         });
         products(IP, 3, [&](int i, int j, bool acc) {
           for (int ks = 0; ks < ksq; ++ks)
-            mma_ts(tm + kColI, tm + kColQ + 64 * i + 8 * ks, mnmajor(sS + j * kPartS, ks),
+            mma_ts(tm + kColI, tm + kColQ + 64 * i, 8 * ks, mnmajor(sS + j * kPartS), mnstep(ks),
                    idesc_bf16(128, 64, 0, 1), acc || ks > 0);
         });
         tc::commit(barA);
@@ -331,7 +315,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
       }
       products(IP, 3, [&](int i, int j, bool acc) {
         for (int ks = 0; ks < ksn; ++ks)
-          mma_ss(tm + kColS, mnmajor(sK + i * kPartK, ks), mnmajor(sX + j * kPartV, ks),
+          mma_ss(tm + kColS, mnmajor(sK + i * kPartK), mnstep(ks), mnmajor(sX + j * kPartV), mnstep(ks),
                  idesc_bf16(NK, 64, 1, 1), acc || ks > 0);
       });
       tc::commit(barB);
@@ -344,7 +328,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
       if (!SUMMARY) load_q(ci + 1);
     }
     if (!SUMMARY) {
-      ok = tc::bar_wait(barA, ph, kBudget) && ok;
+      ok = wait_phase(barA, ph, kBudget) && ok;
       tc::fence_after();
       // P: row i of this thread, 16-column blocks grp and grp + 4, into Q's columns
       const int i = 32 * quad + lane;
@@ -389,7 +373,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
         tc::fence_after();
         products(3, IP, [&](int x, int y, bool acc) {
           for (int ks = 0; ks < ksn; ++ks)
-            mma_ts(tm + kColO, tm + kColQ + 64 * x + 8 * ks, mnmajor(sV + y * kPartV, ks),
+            mma_ts(tm + kColO, tm + kColQ + 64 * x, 8 * ks, mnmajor(sV + y * kPartV), mnstep(ks),
                    idesc_bf16(128, 64, 0, 1), acc || ks > 0);
         });
         tc::commit(barC);
@@ -397,7 +381,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
       }
       __syncwarp();
     }
-    ok = tc::bar_wait(barB, ph, kBudget) && ok;
+    ok = wait_phase(barB, ph, kBudget) && ok;
     tc::fence_after();
     {
       const float dec = sm.pw[n - shift];
@@ -414,7 +398,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
       if (more) put_v(chunk_len(ci + 1));
       continue;
     }
-    ok = tc::bar_wait(barC, ph, kBudget) && ok;
+    ok = wait_phase(barC, ph, kBudget) && ok;
     tc::fence_after();
     if (more) {
       put_v(chunk_len(ci + 1));
@@ -456,7 +440,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
   if (tid == 0 && !ok) {
     atomicExch(a.status, kStatusTimeout);
     for (int i = 0; i < 3; ++i)
-      if (pend[i] >= 0 && !tc::bar_wait(&sm.bar[i], pend[i], kBudget)) atomicExch(a.status, kStatusUndrained);
+      if (pend[i] >= 0 && !wait_phase(&sm.bar[i], pend[i], kBudget)) atomicExch(a.status, kStatusUndrained);
   }
   if (ok && (SUMMARY || (r.fin && last))) {
     const float f = !SUMMARY && len > 0 && r.fin_shift ? sm.pw[1] : 1.f;
