@@ -6,7 +6,7 @@
 // j' counted in walking order, and S [N][64] the state:
 //   A    = Q K^T                      [128 x 128]        tensor cores
 //   Oi   = Q S                        [128 x 64]         tensor cores
-//   P    = intra (A o w)              to bfloat16, kept in tensor memory
+//   P    = intra (A o w)              to bfloat16, kept in tensor memory (mild decays: less its row factor)
 //   out  = inter lam^(i'+1) Oi + P V  [128 x 64]         tensor cores (P from tensor memory)
 //   S'   = lam^n S + K^T V^           V^_j = kv lam^(n-1-j') V_j
 // Rounding: P and the S that multiplies Q go to bfloat16, like the output
@@ -35,6 +35,8 @@
 #include <cudaTypedefs.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "linattn_mma.cuh"
 
 namespace m3 {
@@ -62,14 +64,15 @@ enum Bar {
   kBarB,   // K^T V^ is done
   kBarP,   // P is written and Oi scaled
   kBarC,   // O is done
-  kBarE,   // O is read, the output staged, S written
+  kBarE,  // O is read, S written
+  kBarF,  // the output is staged
   kBarX,   // the staged output has left X
   kBarZ,   // the rows past the sequence's end are zeroed
   kBars
 };
 struct Small {
-  float pw[kC + 4];            // lam^d
-  alignas(16) float col[16];   // column factors of a 16-token block
+  alignas(16) float col[kC];  // column factors of a chunk (mild decays) or of a 16-token block
+  float pw[kC / 2 + 4];       // lam^d, d <= 64
   uint64_t bar[kBars];
   uint32_t tmem;
 };
@@ -117,7 +120,7 @@ __device__ __forceinline__ void tma_store_wait_read() {
 // They meet at mbarriers only (one phase a chunk each, arrivals one a warp), and
 // every wait is bounded, so a thread whose wait gives up leaves the loop and the
 // others follow as theirs do.
-template <int NB, bool SUMMARY, bool REV>
+template <int NB, bool SUMMARY, bool REV, bool MILD>
 __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, int pt, int bh,
                                      int seg, char* raw) {
   constexpr int NK = 64 * NB;
@@ -141,13 +144,16 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
   Small& sm = *reinterpret_cast<Small*>(raw + kTiles);
   if (tid == 0) {
     for (int i = 0; i < kBars; ++i)
-      tc::bar_init(&sm.bar[i], i == kBarW || i == kBarP || i == kBarE || i == kBarZ ? kWarps : 1);
+      tc::bar_init(&sm.bar[i], i == kBarW || i == kBarP || i == kBarE || i == kBarF || i == kBarZ ? kWarps : 1);
     asm volatile("fence.mbarrier_init.release.cluster;");
   }
   const float ld = a.log_decay[h];
-  if (tid <= kC) sm.pw[tid] = la_power(ld, tid);
-  // lam^(15 - j) (walking up: to the block's end) or lam^j (down: to its start)
-  if (tid < 16) sm.col[tid] = la_power(ld, REV ? tid : 15 - tid);
+  if (tid <= kC / 2) sm.pw[tid] = la_power(ld, tid);
+  if (tid < kC) {
+    if (MILD) sm.col[tid] = expf(ld * (float)(REV ? tid - kC / 2 : kC / 2 - tid));
+    else if (tid < 16) sm.col[tid] = la_power(ld, REV ? tid : 15 - tid);
+  }
+  auto power = [&](int d) { return d <= kC / 2 ? sm.pw[d] : sm.pw[kC / 2] * sm.pw[d - kC / 2]; };
   if (warp == 0) tc::tmem_alloc(&sm.tmem, kCols);
 
   // this thread's part of the state: row n = srow, columns p_lo + scol ..
@@ -161,13 +167,18 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
   const int64_t sbase = (int64_t)bh * N * P;
   // chunk c of a row is at the first one's address with c's bits flipped in
   const uint32_t at_state = base + chunk_at(srow, scol / 8);
-  auto put_state = [&]() {
+  // the state that multiplies Q; `f`: MILD, what is common to the chunk's rows
+  auto put_state = [&](float f) {
+    float x[SC];
+#pragma unroll
+    for (int j = 0; j < SC; ++j) x[j] = MILD ? f * st[j] : st[j];
 #pragma unroll
     for (int c = 0; c < SC / 8; ++c)
       sts<kS>(at_state ^ (c << 4),
-          make_uint4(pack(st[8 * c], st[8 * c + 1]), pack(st[8 * c + 2], st[8 * c + 3]),
-                     pack(st[8 * c + 4], st[8 * c + 5]), pack(st[8 * c + 6], st[8 * c + 7])));
+              make_uint4(pack(x[8 * c], x[8 * c + 1]), pack(x[8 * c + 2], x[8 * c + 3]),
+                         pack(x[8 * c + 4], x[8 * c + 5]), pack(x[8 * c + 6], x[8 * c + 7])));
   };
+  const float ratio = MILD ? r.inter / r.intra : 1.f;
   if (warp < kWarps) {
 #pragma unroll
     for (int j = 0; j < SC; ++j) {
@@ -178,7 +189,10 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
         else if (r.init) st[j] = r.init[sbase + (int64_t)p * r.sp + (int64_t)srow * r.sn];
       }
     }
-    if (!SUMMARY) put_state();
+    if (!SUMMARY)
+      put_state(ratio * (!MILD ? 1.f
+                         : !REV ? la_power(ld, kC / 2 + 1)
+                                : expf(ld * (float)(min(kC, ntok - (nchunk - 1) * kC) - (first ? r.shift : 0) - kC / 2))));
   }
   tc::fence_async_smem();
   __syncthreads();
@@ -255,19 +269,22 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
 #pragma unroll
         for (int ks = 0; ks < NK / 16; ++ks)
           if (ks < ksq && lead) mma_ss(tm, dQ, kstep(ks), dK, kstep(ks), idesc_bf16(128, 128, 0, 0), ks > 0);
-        if (ci > 0) {  // the state is in place, the last output read and staged
+        if (ci > 0) {  // the state is in place, the last output read
           if (!wait(kBarE, ph ^ 1)) break;
           tc::fence_after();
-          store(ci - 1);
         }
 #pragma unroll
         for (int ks = 0; ks < NK / 16; ++ks)
           if (ks < ksq && lead)
             mma_ss(tm + kColO, dQ, kstep(ks), dS, mnstep(ks), idesc_bf16(128, 64, 0, 1), ks > 0);
         commit(kBarA, ci);
-        if (ci > 0 && lead) {
-          tma_store_wait_read();
-          tc::bar_arrive(&sm.bar[kBarX]);
+        if (ci > 0) {
+          if (!wait(kBarF, ph ^ 1)) break;
+          store(ci - 1);
+          if (lead) {
+            tma_store_wait_read();
+            tc::bar_arrive(&sm.bar[kBarX]);
+          }
         }
       }
       if (!wait(kBarW, ph)) break;
@@ -300,7 +317,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
         if (more) load_v(ci + 1);
       }
     }
-    if (!SUMMARY && ok && wait(kBarE, (nchunk - 1) & 1)) store(nchunk - 1);
+    if (!SUMMARY && ok && wait(kBarF, (nchunk - 1) & 1)) store(nchunk - 1);
     if (lead) tma_store_wait_read();
     if (!ok) {  // bounded waits for what is still in flight
       if (lead) atomicExch(a.status, kStatusTimeout);
@@ -316,16 +333,18 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
     };
     const int i = 32 * quad + lane;  // this thread's row of A, P and O
     const uint32_t at_v = base + chunk_at(tid >> 2, 2 * (tid & 3)), at_o = base + chunk_at(i, 2 * grp);
-    // row factors of the two blocks of 16 columns; on the diagonal they count
-    // from the far end and may pass one, which a decay of more than e^2.5 a token
-    // (e^77 over the block) forbids: it takes lam^d from the table there
-    const bool mild = ld > -2.5f && ld < 2.5f;
+    // A decay of at most e a token splits into a factor of the row and one of the
+    // column over the whole chunk, lam^(i-j) = lam^(i-64) lam^(64-j), each within
+    // e^64: P takes the column's alone, S the one its readout shares, and the row's
+    // is the output's. Stronger decays take a row factor for every block of 16
+    // columns, and lam^d from the table on the diagonal.
     const float intra = r.intra;
+    const float rowf = MILD ? intra * expf(ld * (float)(REV ? kC / 2 - i : i - kC / 2)) : 1.f;
     float fac[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int c = 32 * grp + 16 * x, d = REV ? c - i : i - c - 15;
-      fac[x] = d < -31 ? 0.f : d < 0 ? intra * expf(ld * (float)d) : intra * sm.pw[d];
+      fac[x] = MILD || d < 0 ? 0.f : intra * power(d);
     }
     for (int ci = 0; ci < nchunk; ++ci) {
       const uint32_t ph = ci & 1;
@@ -346,7 +365,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
       if (!wait(kBarV, ph)) break;
       {
         const int j = tid >> 2;
-        const float w = j < n ? r.kv * sm.pw[REV ? j : n - 1 - j] : 0.f;
+        const float w = j < n ? r.kv * power(REV ? j : n - 1 - j) : 0.f;
         uint4 low[2];
         if (!SUMMARY && ci > 0 && !wait(kBarX, ph ^ 1)) break;  // the last output has left X
 #pragma unroll
@@ -356,9 +375,10 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
           uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = w * lo_f(in[e]), y = w * hi_f(in[e]);
-            hi[e] = pack(x, y);
-            lo[e] = pack(x - lo_f(hi[e]), y - hi_f(hi[e]));
+            const float2 x = __fmul2_rn(make_float2(w, w), make_float2(lo_f(in[e]), hi_f(in[e])));
+            hi[e] = pack(x.x, x.y);
+            const float2 d = __fadd2_rn(x, make_float2(-lo_f(hi[e]), -hi_f(hi[e])));
+            lo[e] = pack(d.x, d.y);
           }
           sts<kX>(at_v ^ (c << 4), make_uint4(hi[0], hi[1], hi[2], hi[3]));
           low[c] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -398,19 +418,21 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
             ld16(tw + c, s);
             tc::tmem_wait_ld();
             const bool full = REV ? c >= 32 * quad + 32 : c < 32 * quad;
-            if (full || mild) {
+            if (MILD || full) {
               const float2 f2 = make_float2(fac[x], fac[x]);
 #pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                const float4 w = *reinterpret_cast<const float4*>(&sm.col[2 * e]);
-                const float2 u = __fmul2_rn(__fmul2_rn(make_float2(s[2 * e], s[2 * e + 1]), f2),
-                                            make_float2(w.x, w.y));
-                const float2 v = __fmul2_rn(__fmul2_rn(make_float2(s[2 * e + 2], s[2 * e + 3]), f2),
-                                            make_float2(w.z, w.w));
-                s[2 * e] = u.x;
-                s[2 * e + 1] = u.y;
-                s[2 * e + 2] = v.x;
-                s[2 * e + 3] = v.y;
+              for (int e = 0; e < 16; e += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(&sm.col[(MILD ? c : 0) + e]);
+                float2 u = __fmul2_rn(make_float2(s[e], s[e + 1]), make_float2(w.x, w.y));
+                float2 v = __fmul2_rn(make_float2(s[e + 2], s[e + 3]), make_float2(w.z, w.w));
+                if (!MILD) {
+                  u = __fmul2_rn(u, f2);
+                  v = __fmul2_rn(v, f2);
+                }
+                s[e] = u.x;
+                s[e + 1] = u.y;
+                s[e + 2] = v.x;
+                s[e + 3] = v.y;
               }
             }
             if (!full) {
@@ -419,7 +441,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const int d = REV ? d0 + e : d0 - e;
-                if (!mild) s[e] *= intra * sm.pw[max(d, 0)];
+                if (!MILD) s[e] *= intra * power(max(d, 0));
                 s[e] = d >= 0 ? s[e] : 0.f;
               }
             }
@@ -428,9 +450,9 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
           }
           st8(tw + 32 * grp + 8 * x, pk);
         }
-        {  // Oi scaled in place, for O to be added
+        if (!MILD) {  // Oi scaled in place, for O to be added
           const int at = max(REV ? n - 1 - i : i, 0);
-          const float f = r.inter * sm.pw[at + 1 - shift];
+          const float f = r.inter * power(at + 1 - shift);
           float o[16];
           ld16(tw + kColO + 16 * grp, o);
           tc::tmem_wait_ld();
@@ -445,7 +467,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
       if (!wait(kBarB, ph)) break;
       tc::fence_after();
       {
-        const float dec = sm.pw[n - shift];
+        const float dec = power(n - shift);
         float kv[SC];
         if constexpr (NB == 2) {
           ld16(tw + kColS + scol, kv);
@@ -455,9 +477,10 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
         tc::tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < SC; ++j) st[j] = fmaf(dec, st[j], kv[j]);
-        if (!SUMMARY) put_state();
+        if (!SUMMARY) put_state(ratio * power(REV ? kC / 2 : kC / 2 + 1));
       }
       tc::fence_before();
+      tc::fence_async_smem();
       if (SUMMARY) continue;
       if (!wait(kBarC, ph)) break;
       tc::fence_after();
@@ -466,6 +489,12 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
         float o[16];
         ld16(tw + kColO + c0, o);
         tc::tmem_wait_ld();
+        tc::fence_before();
+        arrive(kBarE);
+        if (MILD) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] *= rowf;
+        }
         const int64_t at_out = (chunk_row(ci) + i) * r.os + (int64_t)h * P + p_lo + c0;
         if (r.out_rep > 1) {  // float32 partials of a shared head
           if (i < n) {
@@ -485,13 +514,12 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
               *(uint4*)((__nv_bfloat16*)r.out + at_out + 8 * x) = v;
           }
         }
-        tc::fence_before();
         tc::fence_async_smem();
-        arrive(kBarE);
+        arrive(kBarF);
       }
     }
     if (ok && (SUMMARY || (r.fin && last))) {
-      const float f = !SUMMARY && len > 0 && r.fin_shift ? sm.pw[1] : 1.f;
+      const float f = !SUMMARY && len > 0 && r.fin_shift ? power(1) : 1.f;
 #pragma unroll
       for (int j = 0; j < SC; ++j) {
         const int p = p_lo + scol + j;
@@ -524,14 +552,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const int item = x % tiles, unit = x / tiles;
   const int bh = unit % (a.B * a.H), seg = unit / (a.B * a.H);
-  const bool wide = a.role[ri].N > 64;
-  if (a.role[ri].reverse) {
-    if (wide) walk<2, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
-    else walk<1, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
-  } else {
-    if (wide) walk<2, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);
-    else walk<1, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);
-  }
+  const LaRole& r = a.role[ri];
+  const float ld = a.log_decay[bh % a.H], ratio = r.inter / r.intra;
+  const bool mild = fabsf(ld) <= 1.f && fabsf(ratio) < 1e6f && fabsf(ratio) > 1e-6f;  // else: strong, or scale 0
+  auto go = [&](auto nb, auto rev) {
+    if (mild && !SUMMARY) walk<nb.value, SUMMARY, rev.value, true>(a, maps, ri, item, bh, seg, raw);
+    else walk<nb.value, SUMMARY, rev.value, false>(a, maps, ri, item, bh, seg, raw);
+  };
+  auto by_way = [&](auto nb) {
+    if (r.reverse) go(nb, std::true_type());
+    else go(nb, std::false_type());
+  };
+  if (r.N > 64) by_way(std::integral_constant<int, 2>());
+  else by_way(std::integral_constant<int, 1>());
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {

@@ -6,34 +6,46 @@ namespace m3 {
 namespace {
 
 // Entry states of the segments from their own sums, in walking order: one
-// thread per state element.
-__global__ void __launch_bounds__(256) k_la_prefix(LaArgs a) {
+// thread per state element, the sums of eight segments in flight at a time.
+__global__ void __launch_bounds__(256) k_la_prefix(const __grid_constant__ LaArgs a) {
+  constexpr int kAhead = 8;
   const int bh = blockIdx.x % (a.B * a.H), ri = blockIdx.x / (a.B * a.H);
   const LaRole& r = a.role[ri];
-  const int i = blockIdx.y * 256 + threadIdx.x;
-  if (i >= r.N * r.P) return;
+  const int np = r.N * r.P, i = blockIdx.y * 256 + threadIdx.x;
+  if (i >= np) return;
   int64_t row0, len;
   la_rows(a, bh / a.H, &row0, &len);
   const float ld = a.log_decay[bh % a.H];
   const int last = len > 0 ? (int)((len - 1) / a.seg_len) : 0;
   const int p = i / r.N, n = i - p * r.N;
-  float st = r.init ? r.init[(int64_t)bh * r.N * r.P + (int64_t)p * r.sp + n * r.sn] : 0.f;
-  const int64_t step = (int64_t)a.B * a.H * r.N * r.P;
-  float* e = a.entry + ri * a.entry_role + (int64_t)bh * r.N * r.P + i;
-  for (int x = 0; x <= last; ++x) {
-    const int seg = r.reverse ? last - x : x;
-    float* at = e + seg * step;
-    const float own = x < last ? *at : 0.f;
-    *at = st;
-    const int64_t n_tok = min(a.seg_len, len - seg * a.seg_len) - (x == 0 ? r.shift : 0);
-    if (x < last) st = la_power(ld, n_tok) * st + own;
+  float st = r.init ? r.init[(int64_t)bh * np + (int64_t)p * r.sp + (int64_t)n * r.sn] : 0.f;
+  const int64_t step = (int64_t)a.B * a.H * np;
+  float* e = a.entry + ri * a.entry_role + (int64_t)bh * np + i;
+  // every segment but the sequence's last rows' one has seg_len tokens
+  const float whole = la_power(ld, a.seg_len), tail = la_power(ld, len - last * a.seg_len);
+  for (int x0 = 0; x0 <= last; x0 += kAhead) {
+    float own[kAhead];
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const int x = x0 + y;
+      own[y] = x < last ? e[(r.reverse ? last - x : x) * step] : 0.f;
+    }
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const int x = x0 + y, seg = r.reverse ? last - x : x;
+      if (x > last) break;
+      e[seg * step] = st;
+      float dec = seg == last ? tail : whole;
+      if (x == 0 && r.shift) dec = la_power(ld, (seg == last ? len - last * a.seg_len : a.seg_len) - 1);
+      st = fmaf(dec, st, own[y]);
+    }
   }
 }
 
 // One row a block. With offsets, rows of no sequence keep what they hold.
 template <typename T>
 __global__ void __launch_bounds__(128)
-    k_la_group_sum(LaArgs a, const float* part, T* out, int groups, int rep, int width) {
+    k_la_group_sum(const __grid_constant__ LaArgs a, const float* part, T* out, int groups, int rep, int width) {
   const int64_t row = blockIdx.x;
   if (a.offsets) {
     int lo = 0, hi = a.B;  // the last sequence that begins at or before the row

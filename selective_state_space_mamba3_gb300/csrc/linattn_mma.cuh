@@ -71,9 +71,13 @@ __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // Byte offset of the 16-byte chunk `c` of row r in a swizzled block.
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
-// Bounded wait; the clock is read only where the first try fails.
+// Bounded wait. One try nearly always sees the phase end; what follows where it
+// does not stays out of line, out of the way of the instruction cache.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t phase, long long budget) {
+  return tc::bar_wait(bar, phase, budget);
+}
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t phase, long long budget) {
-  return tc::bar_try(bar, phase) || tc::bar_wait(bar, phase, budget);
+  return tc::bar_try(bar, phase) || wait_on(bar, phase, budget);
 }
 // Shared-memory words at a register's address plus a constant, so that the tiles'
 // addresses do not take a register each.
