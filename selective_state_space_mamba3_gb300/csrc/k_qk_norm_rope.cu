@@ -22,26 +22,39 @@ namespace m3 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBwdBlocks = 608;  // four blocks on each of 152 SMs
+constexpr int kBwdBlocks = 304;  // two blocks on each of 152 SMs
 constexpr int kMaxD = 256;
 
+// Eight values as they lie in memory, and as float32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* v);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float* v) {
-  const float4 a = *(const float4*)p, b = *(const float4*)(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+struct Raw {
+  uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load8(const T* p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    *reinterpret_cast<uint4*>(r.w + 4 * i) = *(reinterpret_cast<const uint4*>(p) + i);
+  return r;
 }
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float* v) {
-  const uint4 r = *(const uint4*)p;
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+__device__ __forceinline__ void values(const Raw<float>& r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+}
+__device__ __forceinline__ void values(const Raw<__nv_bfloat16>& r, float* v) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    v[2 * i] = __uint_as_float(r.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
   }
+}
+template <typename T>
+__device__ __forceinline__ Raw<T> from_lane(const Raw<T>& r, int lane) {
+  Raw<T> o;
+#pragma unroll
+  for (int i = 0; i < 2 * (int)sizeof(T); ++i) o.w[i] = __shfl_sync(0xffffffffu, r.w[i], lane);
+  return o;
 }
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float* v);
@@ -71,107 +84,143 @@ __device__ __forceinline__ int table_row(const RopeArgs& a, int64_t row) {
   return p >= 0 && p < a.max_pos ? (int)p : -1;
 }
 
-// Adds the weight-gradient sums that every thread holds for its columns of
-// both sides (gw[side][i], column col + i) over the block and writes them to
-// the block's slot of `partial` [block][2][D].
+// Blocks of a launch: the first `q_blocks` take queries, the rest keys.
+struct Split {
+  int q_blocks, blocks;
+};
+__device__ __forceinline__ int side_of(const Split& p) { return (int)blockIdx.x >= p.q_blocks; }
+__device__ __forceinline__ int index_in(const Split& p) { return side_of(p) ? blockIdx.x - p.q_blocks : blockIdx.x; }
+__device__ __forceinline__ int blocks_of(const Split& p) { return side_of(p) ? p.blocks - p.q_blocks : p.q_blocks; }
+
+// Adds the weight-gradient sums that every thread holds for its columns
+// (cols[i], -1: none) over the block's `slots` in order and writes them to the
+// block's row of `partial` [block][D].
 template <int W>
-__device__ __forceinline__ void block_weights(const RopeArgs& a, float gw[2][W], int slot, int slots,
+__device__ __forceinline__ void block_weights(const RopeArgs& a, const float* gw, int slot, int slots,
                                               const int* cols) {
   extern __shared__ float sm[];
-#pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    __syncthreads();
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (cols[i] >= 0) sm[slot * a.D + cols[i]] = gw[side][i];
-    __syncthreads();
-    for (int d = threadIdx.x; d < a.D; d += kThreads) {
-      float s = 0.f;
-      for (int x = 0; x < slots; ++x) s += sm[x * a.D + d];
-      a.partial[((int64_t)blockIdx.x * 2 + side) * a.D + d] = s;
-    }
+  for (int i = 0; i < W; ++i)
+    if (cols[i] >= 0) sm[slot * a.D + cols[i]] = gw[i];
+  __syncthreads();
+  for (int d = threadIdx.x; d < a.D; d += kThreads) {
+    float s = 0.f;
+    for (int x = 0; x < slots; ++x) s += sm[x * a.D + d];
+    a.partial[(int64_t)blockIdx.x * a.D + d] = s;
   }
 }
 
 // Eight consecutive values a lane. `per`: heads of one row that a lane group
-// takes in turn; an item is (row, run of `per` heads of one side).
+// takes, kAhead at a time with their loads in flight together; an item is (row,
+// run of `per` heads). With inv the inverse RMS the forward pass is
+// y_i = inv (x_i wc_i + xm_i ws_i), xm the value A away (from lane `mate`), wc = w
+// cos and ws = +-w_m sin the same for every head of the row.
 template <typename T, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD ? 3 : 4)
-    k_rope_vec(RopeArgs a, int lanes, int per, int64_t items) {
+__global__ void __launch_bounds__(kThreads, BWD ? 2 : 4)
+    k_rope_vec(const __grid_constant__ RopeArgs a, Split split, int lanes, int per) {
+  constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
   const int lane = threadIdx.x & 31, li = lane % lanes, base = lane - li;
   const int grp = threadIdx.x / lanes, ngrp = kThreads / lanes;
   const int D = a.D, A = a.A, e = 8 * li;
   const bool on = e < D;
   // the lane that holds the other half of this lane's pairs, and the sign of its term
-  const int mate = e < A ? base + li + A / 8 : e < 2 * A ? base + li - A / 8 : lane;
+  const int em = e < A ? e + A : e < 2 * A ? e - A : e;  // that half's values
+  const int mate = base + em / 8;
   const float sign = (e < A ? -1.f : 1.f) * (BWD ? -1.f : 1.f);
-  const int runs0 = (a.side[0].heads + per - 1) / per, runs1 = (a.side[1].heads + per - 1) / per;
-  const int runs = runs0 + runs1;
+  const int sd = side_of(split);
+  const RopeSide& s = a.side[sd];
+  const int runs = (s.heads + per - 1) / per;
+  const int64_t items = a.rows * runs;
   const float inv_d = 1.0f / (float)D;
-  float gw[2][8] = {};
+  float gw[8] = {};
   // whole warps leave the loop together: the shuffles below name all 32 lanes
-  const int64_t stride = (int64_t)gridDim.x * ngrp;
-  for (int64_t it0 = (int64_t)blockIdx.x * ngrp + (grp - base / lanes); it0 < items; it0 += stride) {
+  const int64_t stride = (int64_t)blocks_of(split) * ngrp;
+  for (int64_t it0 = (int64_t)index_in(split) * ngrp + (grp - base / lanes); it0 < items; it0 += stride) {
     const int64_t it = it0 + base / lanes;
     const bool live = it < items;
     const int64_t row = live ? it / runs : 0;
     const int run = live ? (int)(it - row * runs) : 0;
-    const int sd = run >= runs0;
-    const RopeSide& s = a.side[sd];
-    const int h0 = (sd ? run - runs0 : run) * per, h1 = live ? min(s.heads, h0 + per) : h0;
+    const int h0 = run * per, h1 = live && on ? min(s.heads, h0 + per) : h0;
+    const T* x = (const T*)s.x + row * s.xs + e;
+    const T* dy = (const T*)s.dy + row * s.dys + e;
+    T* y = (T*)s.y + row * s.ys + e;
+    Raw<T> rx[kAhead], rg[BWD ? kAhead : 1];
+    auto load = [&](int hb) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int h = h0 + hb + u;
+        rx[u] = Raw<T>{};
+        if (BWD) rg[BWD ? u : 0] = Raw<T>{};
+        if (h < h1 && hb + u < per) {
+          rx[u] = load8(x + h * D);
+          if (BWD) rg[BWD ? u : 0] = load8(dy + h * D);
+        }
+      }
+    };
+    load(0);  // before the position, which the tables wait for
     float c[8], sn[8], w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) { c[i] = 1.f; sn[i] = 0.f; w[i] = 1.f; }
     const int tr = live ? table_row(a, row) : -1;
     if (tr >= 0 && e < 2 * A) {
       const int64_t at = (int64_t)tr * A + (e < A ? e : e - A);
-      load8(a.cos_table + at, c);
-      load8(a.sin_table + at, sn);
+      values(load8(a.cos_table + at), c);
+      values(load8(a.sin_table + at), sn);
     }
-    if (on && s.w) load8(s.w + e, w);
-    const T* x = (const T*)s.x + row * s.xs + e;
-    const T* dy = (const T*)s.dy + row * s.dys + e;
-    T* y = (T*)s.y + row * s.ys + e;
-    for (int hh = 0; hh < per; ++hh) {
-      const int h = h0 + hh;
-      const bool in = on && h < h1;
-      float v[8] = {}, g[8] = {};
-      if (in) {
-        load8(x + h * D, v);
-        if (BWD) load8(dy + h * D, g);
-      }
-      float ss = 0.f;
+    if (on && s.w) values(load8(s.w + e), w);
+    float wm[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-      ss = group_sum(ss, lanes);
-      const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
-      if (!BWD) {
+    for (int i = 0; i < 8; ++i) wm[i] = 1.f;
+    if (!BWD && on && s.w) values(load8(s.w + em), wm);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] * inv * w[i];
-      }
-      if (A > 0) {
+    for (int i = 0; i < 8; ++i) {
+      if (!BWD) c[i] *= w[i];
+      sn[i] *= BWD ? sign : sign * wm[i];
+    }
+    for (int hb = 0; hb < per; hb += kAhead) {
+      if (hb > 0) load(hb);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float& t = BWD ? g[i] : v[i];
-          const float o = __shfl_sync(0xffffffffu, t, mate);
-          t = fmaf(t, c[i], sign * o * sn[i]);
+      for (int u = 0; u < kAhead; ++u) {
+        const int h = h0 + hb + u;
+        const bool in = h < h1 && hb + u < per;
+        float v[8], m[8];
+        values(rx[u], v);
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
+        ss = group_sum(ss, lanes);
+        const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
+        if (!BWD) {
+          if (A > 0) {
+            values(from_lane(rx[u], mate), m);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = inv * fmaf(m[i], sn[i], v[i] * c[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = inv * (v[i] * c[i]);
+          }
+        } else {
+          float g[8];
+          values(rg[BWD ? u : 0], g);
+          if (A > 0) {
+            values(from_lane(rg[BWD ? u : 0], mate), m);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = fmaf(m[i], sn[i], g[i] * c[i]);
+          }
+          float dot = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i] *= inv;
+            gw[i] = fmaf(g[i], v[i], gw[i]);
+            g[i] *= w[i];
+            dot = fmaf(g[i], v[i], dot);
+          }
+          dot = group_sum(dot, lanes) * inv_d;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = inv * fmaf(-v[i], dot, g[i]);
         }
+        if (in) store8(y + h * D, v);
       }
-      if (BWD) {
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] *= inv;
-          if (sd) gw[1][i] = fmaf(g[i], v[i], gw[1][i]);
-          else gw[0][i] = fmaf(g[i], v[i], gw[0][i]);
-          g[i] *= w[i];
-          dot = fmaf(g[i], v[i], dot);
-        }
-        dot = group_sum(dot, lanes) * inv_d;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = inv * fmaf(-v[i], dot, g[i]);
-      }
-      if (in) store8(y + h * D, v);
     }
   }
   if constexpr (BWD) {
@@ -187,11 +236,13 @@ __global__ void __launch_bounds__(kThreads, BWD ? 3 : 4)
 // Any width and alignment: one warp per head; a lane holds pairs (a, a + A),
 // a = lane + 32 i, and unrotated values 2A + lane + 32 i.
 template <typename T, bool BWD>
-__global__ void __launch_bounds__(kThreads) k_rope_any(RopeArgs a, int64_t items) {
+__global__ void __launch_bounds__(kThreads) k_rope_any(const __grid_constant__ RopeArgs a, Split split) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kPairs = kMaxD / 64, kRest = kMaxD / 32;
   const int D = a.D, A = a.A;
-  const int heads = a.side[0].heads + a.side[1].heads;
+  const int sd = side_of(split);
+  const RopeSide& s = a.side[sd];
+  const int64_t items = a.rows * s.heads;
   const float inv_d = 1.0f / (float)D;
   constexpr int W = 2 * kPairs + kRest;
   int cols[W];
@@ -206,13 +257,10 @@ __global__ void __launch_bounds__(kThreads) k_rope_any(RopeArgs a, int64_t items
     const int d = 2 * A + lane + 32 * i;
     cols[2 * kPairs + i] = d < D ? d : -1;
   }
-  float gw[2][W] = {};
-  for (int64_t it = (int64_t)blockIdx.x * 8 + warp; it < items; it += (int64_t)gridDim.x * 8) {
-    const int64_t row = it / heads;
-    const int hh = (int)(it - row * heads);
-    const int sd = hh >= a.side[0].heads;
-    const RopeSide& s = a.side[sd];
-    const int h = sd ? hh - a.side[0].heads : hh;
+  float gw[W] = {};
+  for (int64_t it = (int64_t)index_in(split) * 8 + warp; it < items; it += (int64_t)blocks_of(split) * 8) {
+    const int64_t row = it / s.heads;
+    const int h = (int)(it - row * s.heads);
     const T* x = (const T*)s.x + row * s.xs + (int64_t)h * D;
     const T* dy = (const T*)s.dy + row * s.dys + (int64_t)h * D;
     T* y = (T*)s.y + row * s.ys + (int64_t)h * D;
@@ -250,8 +298,7 @@ __global__ void __launch_bounds__(kThreads) k_rope_any(RopeArgs a, int64_t items
 #pragma unroll
       for (int i = 0; i < W; ++i) {
         v[i] *= inv;
-        if (sd) gw[1][i] = fmaf(g[i], v[i], gw[1][i]);
-        else gw[0][i] = fmaf(g[i], v[i], gw[0][i]);
+        gw[i] = fmaf(g[i], v[i], gw[i]);
         g[i] *= s.w && cols[i] >= 0 ? s.w[cols[i]] : 1.f;
         dot = fmaf(g[i], v[i], dot);
       }
@@ -269,17 +316,18 @@ __global__ void __launch_bounds__(kThreads) k_rope_any(RopeArgs a, int64_t items
 }
 
 // Weight gradients from the blocks' sums: 32 columns a block, each of its
-// eight warps a run of the blocks in order, then the warps in order.
-__global__ void __launch_bounds__(256) k_rope_weights(RopeArgs a, int blocks) {
+// eight warps a run of the side's blocks in order, then the warps in order.
+__global__ void __launch_bounds__(256) k_rope_weights(const __grid_constant__ RopeArgs a, Split split) {
   __shared__ float part[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int side = blockIdx.y, d = blockIdx.x * 32 + lane;
   if (!a.gw[side]) return;
-  const int per = (blocks + 7) / 8;
+  const int first = side ? split.q_blocks : 0, end = side ? split.blocks : split.q_blocks;
+  const int per = (end - first + 7) / 8;
   float s = 0.f;
   if (d < a.D)
-    for (int x = warp * per; x < min(blocks, (warp + 1) * per); ++x)
-      s += a.partial[((int64_t)x * 2 + side) * a.D + d];
+    for (int x = first + warp * per; x < min(end, first + (warp + 1) * per); ++x)
+      s += a.partial[(int64_t)x * a.D + d];
   part[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && d < a.D) {
@@ -303,36 +351,41 @@ bool vec_ok(const RopeArgs& a, bool bwd) {
   return true;
 }
 
+// At most `most` blocks (one more where a side has few) of `step` items, in the
+// two sides' proportion.
+Split divide(int64_t q_items, int64_t k_items, int step, int64_t most) {
+  int64_t q = (q_items + step - 1) / step, k = (k_items + step - 1) / step;
+  if (q + k > most) {
+    const int64_t all = q + k;
+    if (q > 0) q = q * most / all > 0 ? q * most / all : 1;
+    if (k > 0) k = most - q > 0 ? most - q : 1;
+  }
+  return {(int)q, (int)(q + k)};
+}
+
 template <typename T, bool BWD>
 cudaError_t go(const RopeArgs& a, cudaStream_t s) {
-  const int heads = a.side[0].heads + a.side[1].heads;
-  unsigned grid;
+  Split split;
   if (vec_ok(a, BWD)) {
     int lanes = 1;
     while (lanes * 8 < a.D) lanes *= 2;
     const int ngrp = kThreads / lanes;
     // heads a lane group: as many as leave every SM several blocks
-    int per = 8;
-    auto count = [&](int p) {
-      return a.rows * ((a.side[0].heads + p - 1) / p + (a.side[1].heads + p - 1) / p);
-    };
-    while (per > 1 && count(per) < (int64_t)152 * 8 * ngrp) per /= 2;
-    const int64_t items = count(per), blocks = (items + ngrp - 1) / ngrp;
-    const int64_t most = BWD ? kBwdBlocks : 152 * 4 * 8;
-    grid = (unsigned)(blocks < most ? blocks : most);
+    int per = BWD ? 8 : 16;
+    auto runs = [&](int side) { return a.rows * ((a.side[side].heads + per - 1) / per); };
+    while (per > 1 && runs(0) + runs(1) < (int64_t)152 * 8 * ngrp) per /= 2;
+    split = divide(runs(0), runs(1), ngrp, BWD ? kBwdBlocks : 152 * 4 * 8);
     const size_t smem = BWD && a.partial ? (size_t)ngrp * a.D * sizeof(float) : 0;
-    k_rope_vec<T, BWD><<<grid, kThreads, smem, s>>>(a, lanes, per, items);
+    k_rope_vec<T, BWD><<<(unsigned)split.blocks, kThreads, smem, s>>>(a, split, lanes, per);
   } else {
-    const int64_t items = a.rows * heads, blocks = (items + 7) / 8;
-    const int64_t most = BWD ? kBwdBlocks : 152 * 8 * 8;
-    grid = (unsigned)(blocks < most ? blocks : most);
+    split = divide(a.rows * a.side[0].heads, a.rows * a.side[1].heads, 8, BWD ? kBwdBlocks : 152 * 8 * 8);
     const size_t smem = BWD && a.partial ? (size_t)8 * a.D * sizeof(float) : 0;
-    k_rope_any<T, BWD><<<grid, kThreads, smem, s>>>(a, items);
+    k_rope_any<T, BWD><<<(unsigned)split.blocks, kThreads, smem, s>>>(a, split);
   }
   count_launches(1);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !BWD || !a.partial) return e;
-  k_rope_weights<<<dim3((unsigned)((a.D + 31) / 32), 2), 256, 0, s>>>(a, (int)grid);
+  k_rope_weights<<<dim3((unsigned)((a.D + 31) / 32), 2), 256, 0, s>>>(a, split);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -343,7 +396,7 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t s) {
   return a.dtype == M3_DTYPE_FP32 ? go<float, false>(a, s) : go<__nv_bfloat16, false>(a, s);
 }
 size_t qk_norm_rope_backward_bytes(const RopeArgs& a) {
-  return (size_t)kBwdBlocks * 2 * a.D * sizeof(float);
+  return (size_t)(kBwdBlocks + 1) * a.D * sizeof(float);
 }
 cudaError_t launch_qk_norm_rope_backward(const RopeArgs& a, cudaStream_t s) {
   return a.dtype == M3_DTYPE_FP32 ? go<float, true>(a, s) : go<__nv_bfloat16, true>(a, s);
