@@ -12,9 +12,9 @@
 // Q are the tensor-memory operand of A = Q K^T and Oi = Q S (rows 112..127 of
 // the 128-row tile stay zero), and the parts of P take their columns after
 // both, so tensor memory is full: Q / P 192, A 128, O, Oi and K^T V^ 64 each.
-// One block of 512 threads an SM; the next chunk's rows are loaded into
-// registers while this one's products run, and cut and stored to shared memory
-// as soon as the product that read the tile is done.
+// One block an SM. While the products of a chunk run, the next chunk's rows are
+// fetched into L2; K's are cut and stored as soon as K^T V^ has read the tile, those
+// of Q and V as soon as P V has.
 //
 // Bound by the tensor cores: six passes cost 6,900 cycles a chunk at N = 128,
 // P = 64, against 7,300 for its bytes at the HBM rate.
@@ -24,7 +24,8 @@ namespace m3 {
 namespace {
 
 constexpr int kC = 112;
-constexpr int kThreads = 512;
+constexpr int kWarps = 16;  // compute warps; one more issues
+constexpr int kThreads = 32 * (kWarps + 1);
 constexpr long long kBudget = 4000000000LL;  // clock cycles, about 2 s
 constexpr uint32_t kBlk = kC * 128;          // bytes of a 64-column block of a tile part
 constexpr int kParts = 3;
@@ -34,10 +35,19 @@ __host__ __device__ constexpr uint32_t state_bytes(int nb) { return nb * 8192; }
 __host__ __device__ constexpr uint32_t tile_bytes(int nb) {
   return kParts * (nb * kBlk + 2 * kBlk + state_bytes(nb));
 }
+enum Bar {
+  kBarQ,  // Q, K and S are in place, O and Oi read
+  kBarX,  // V and V^ are in place
+  kBarA,  // A and Oi are done
+  kBarB,  // K^T V^ is done
+  kBarP,  // P is written
+  kBarC,  // O is done
+  kBars
+};
 struct Small {
-  float pw[kC + 20];  // lam^d, d <= 128
-  float col[16];      // column factors of a 16-token block
-  uint64_t bar[3];
+  alignas(16) float col[16];  // column factors of a 16-token block
+  float pw[kC + 20];          // lam^d, d <= 128
+  uint64_t bar[kBars];
   uint32_t tmem;
 };
 static_assert(sizeof(Small) <= 1024, "");
@@ -60,9 +70,6 @@ __device__ __forceinline__ void cut2(float a, float b, uint32_t* p) {
   a -= top(a);
   b -= top(b);
   p[2] = pair_top(a, b);
-}
-__device__ __forceinline__ void sts2(uint32_t a, uint32_t x, uint32_t y) {
-  asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 // Byte offset of the four elements at column c (c % 4 == 0) of row r of a part
 // with 64-column blocks of kBlk bytes.
@@ -110,348 +117,426 @@ __device__ __forceinline__ bool vec_rows(const void* p, int width, int64_t strid
   return width % 4 == 0 && stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0;
 }
 
-// One block's walk (see k_linattn_mma.cu). NB: 64-column blocks of N.
-template <typename T, int NB, bool SUMMARY>
+// One block's walk (see k_linattn_mma.cu: warps 0..15 compute, one lane of warp 16
+// issues the products, and they meet at mbarriers with bounded waits). NB:
+// 64-column blocks of N.
+template <typename T, int NB, bool SUMMARY, bool REV>
 __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, int seg, char* raw) {
   constexpr int IP = sizeof(T) == 4 ? 3 : 1;  // parts of an input
   constexpr int NK = 64 * NB;
-  constexpr int SC = NB == 2 ? 16 : 8;                     // state columns a thread
-  constexpr int KQ = (kC * NK / 4 + kThreads - 1) / kThreads;  // quads of K a thread
-  constexpr int VQ = (kC * 16 + kThreads - 1) / kThreads;      // quads of V a thread
+  constexpr int SC = NB == 2 ? 16 : 8;                             // state columns a thread
+  constexpr int KQ = (kC * NK / 4 + 32 * kWarps - 1) / (32 * kWarps);  // quads of K a thread
+  constexpr int VQ = (kC * 16 + 32 * kWarps - 1) / (32 * kWarps);      // quads of V a thread
   const LaRole& r = a.role[ri];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quad = warp & 3, grp = warp >> 2;
+  const int quad = warp & 3, grp = (warp >> 2) & 3;
   const int b = bh / a.H, h = bh - b * a.H;
   const int N = r.N, P = r.P, p_lo = 64 * pt;
-  int64_t row0, len;
-  la_rows(a, b, &row0, &len);
-  const int64_t s0 = seg * a.seg_len, s1 = min(len, s0 + a.seg_len);
-  const int64_t last_seg = len > 0 ? (len - 1) / a.seg_len : 0;
+  int64_t seq0, len;
+  la_rows(a, b, &seq0, &len);
+  const int last_seg = len > 0 ? (int)((len - 1) / a.seg_len) : 0;
   if (seg > last_seg) return;
-  if (SUMMARY && seg == (r.reverse ? 0 : last_seg)) return;  // the prefix pass never reads it
-  const bool first = seg == (r.reverse ? last_seg : 0), last = seg == (r.reverse ? 0 : last_seg);
-  const int nchunk = s1 > s0 ? (int)((s1 - s0 + kC - 1) / kC) : 0;
-  const T* gq = (const T*)r.q + (int64_t)(h / r.q_rep) * N;
-  const T* gk = (const T*)r.k + (int64_t)(h / r.k_rep) * N;
-  const T* gv = (const T*)r.v + (int64_t)(h / r.v_rep) * P;
-  const bool qvec = vec_rows<T>(gq, N, r.qs), kvec = vec_rows<T>(gk, N, r.ks),
-             vvec = vec_rows<T>(gv, P, r.vs);
+  const int row0 = (int)(seq0 + seg * a.seg_len);  // the segment's rows
+  const int ntok = (int)min(len - seg * a.seg_len, a.seg_len);
+  if (SUMMARY && seg == (REV ? 0 : last_seg)) return;  // the prefix pass never reads it
+  const bool first = seg == (REV ? last_seg : 0), last = seg == (REV ? 0 : last_seg);
+  const int nchunk = (ntok + kC - 1) / kC;
 
   const uint32_t base = tc::smem_u32(raw);
   constexpr uint32_t kPartK = NB * kBlk, kPartV = kBlk, kPartS = state_bytes(NB);
   const uint32_t sK = base, sV = sK + kParts * kPartK, sX = sV + kParts * kPartV,
                  sS = sX + kParts * kPartV;
   Small& sm = *reinterpret_cast<Small*>(raw + tile_bytes(2));
-  uint64_t *barA = &sm.bar[0], *barB = &sm.bar[1], *barC = &sm.bar[2];
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) tc::bar_init(&sm.bar[i], 1);
+    for (int i = 0; i < kBars; ++i) tc::bar_init(&sm.bar[i], i == kBarQ || i == kBarX || i == kBarP ? kWarps : 1);
     asm volatile("fence.mbarrier_init.release.cluster;");
   }
   const float ld = a.log_decay[h];
   if (tid < kC + 20) sm.pw[tid] = la_power(ld, tid);
-  if (tid < 16) sm.col[tid] = la_power(ld, r.reverse ? tid : 15 - tid);
+  if (tid < 16) sm.col[tid] = la_power(ld, REV ? tid : 15 - tid);
   if (warp == 0) tc::tmem_alloc(&sm.tmem, kCols);
   __syncthreads();
   const uint32_t tm = sm.tmem, tw = tm + ((uint32_t)(32 * quad) << 16);
-
-  auto chunk_row = [&](int ci) { return s0 + (int64_t)(r.reverse ? nchunk - 1 - ci : ci) * kC; };
-  auto chunk_len = [&](int ci) { return (int)min((int64_t)kC, s1 - chunk_row(ci)); };
-  // this thread's rows of the next chunk
-  float4 rk[KQ], rv[VQ], rq[NB * 4];
-  auto load_k = [&](int ci) {
-    const T* g = gk + (row0 + chunk_row(ci)) * r.ks;
-    const int n = chunk_len(ci);
-#pragma unroll
-    for (int x = 0; x < KQ; ++x) {
-      const int e = tid + x * kThreads, t = e / (NK / 4), c = e % (NK / 4) * 4;
-      rk[x] = t < n ? load4<T>(g + t * r.ks, c, N, kvec) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  };
-  auto load_v = [&](int ci) {
-    const T* g = gv + (row0 + chunk_row(ci)) * r.vs;
-    const int n = chunk_len(ci);
-#pragma unroll
-    for (int x = 0; x < VQ; ++x) {
-      const int e = tid + x * kThreads, t = e / 16, c = p_lo + e % 16 * 4;
-      rv[x] = t < n ? load4<T>(g + t * r.vs, c, P, vvec) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-  };
-  // queries: tensor-memory row 32 quad + lane, columns NB * 16 grp ..
-  auto load_q = [&](int ci) {
-    const int t = 32 * quad + lane;
-    const T* g = gq + (row0 + chunk_row(ci) + t) * r.qs;
-    const bool in = t < chunk_len(ci);
-#pragma unroll
-    for (int x = 0; x < NB * 4; ++x)
-      rq[x] = in ? load4<T>(g, NB * 16 * grp + 4 * x, N, qvec) : make_float4(0.f, 0.f, 0.f, 0.f);
-  };
-  auto put_k = [&]() {
-#pragma unroll
-    for (int x = 0; x < KQ; ++x) {
-      const int e = tid + x * kThreads, t = e / (NK / 4), c = e % (NK / 4) * 4;
-      if (t >= kC) continue;
-      uint32_t lo[3], hi[3];
-      cut2(rk[x].x, rk[x].y, lo);
-      cut2(rk[x].z, rk[x].w, hi);
-#pragma unroll
-      for (int p = 0; p < IP; ++p) sts2(sK + p * kPartK + quad_at(t, c), lo[p], hi[p]);
-    }
-  };
-  auto put_v = [&](int n) {  // V and V^
-#pragma unroll
-    for (int x = 0; x < VQ; ++x) {
-      const int e = tid + x * kThreads, t = e / 16, c = e % 16 * 4;
-      if (t >= kC) continue;
-      uint32_t lo[3], hi[3];
-      if (!SUMMARY) {
-        cut2(rv[x].x, rv[x].y, lo);
-        cut2(rv[x].z, rv[x].w, hi);
-#pragma unroll
-        for (int p = 0; p < IP; ++p) sts2(sV + p * kPartV + quad_at(t, c), lo[p], hi[p]);
-      }
-      const float w = t < n ? r.kv * sm.pw[r.reverse ? t : n - 1 - t] : 0.f;
-      cut2(w * rv[x].x, w * rv[x].y, lo);
-      cut2(w * rv[x].z, w * rv[x].w, hi);
-#pragma unroll
-      for (int p = 0; p < 3; ++p) sts2(sX + p * kPartV + quad_at(t, c), lo[p], hi[p]);
-    }
-  };
-  auto put_q = [&]() {
-#pragma unroll
-    for (int y = 0; y < NB; ++y) {
-      uint32_t pc[8][3];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        cut2(rq[4 * y + x].x, rq[4 * y + x].y, pc[2 * x]);
-        cut2(rq[4 * y + x].z, rq[4 * y + x].w, pc[2 * x + 1]);
-      }
-#pragma unroll
-      for (int p = 0; p < IP; ++p) {
-        uint32_t v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = pc[e][p];
-        st8(tw + kColQ + 64 * p + NB * 8 * grp + 8 * y, v);
-      }
-    }
-    tc::tmem_wait_st();
-  };
-
-  const int srow = NB == 2 ? 32 * quad + lane : 16 * quad + (lane & 15);
-  const int scol = NB == 2 ? 16 * grp : 16 * grp + 8 * (lane >> 4);
-  float st[SC];
-  float* entry = a.entry ? a.entry + ri * a.entry_role +
-                               ((int64_t)seg * a.B * a.H + bh) * ((int64_t)N * P)
-                         : nullptr;
-  const int64_t sbase = (int64_t)bh * N * P;
-#pragma unroll
-  for (int j = 0; j < SC; ++j) {
-    const int p = p_lo + scol + j;
-    st[j] = 0.f;
-    if (!SUMMARY && srow < N && p < P) {
-      if (a.nseg > 1) st[j] = entry[(int64_t)p * N + srow];
-      else if (r.init) st[j] = r.init[sbase + (int64_t)p * r.sp + (int64_t)srow * r.sn];
-    }
-  }
-  auto put_state = [&]() {
-    uint32_t pc[SC / 2][3];
-#pragma unroll
-    for (int j = 0; j < SC / 2; ++j) cut2(st[2 * j], st[2 * j + 1], pc[j]);
-#pragma unroll
-    for (int p = 0; p < 3; ++p)
-#pragma unroll
-      for (int c = 0; c < SC / 8; ++c)
-        sts(sS + p * kPartS + chunk_at(srow, scol / 8 + c),
-            make_uint4(pc[4 * c][p], pc[4 * c + 1][p], pc[4 * c + 2][p], pc[4 * c + 3][p]));
-  };
   bool ok = true;
-  int pend[3] = {-1, -1, -1};  // thread 0: phases it still has to see end
-  if (nchunk > 0) {
-    load_k(0);
-    load_v(0);
-    if (!SUMMARY) load_q(0);
-    put_k();
-    put_v(chunk_len(0));
-    if (!SUMMARY) put_q();
-  }
-  if (!SUMMARY) put_state();
-  // pairs of parts of a product with `xa` and `xb` parts, the largest last
-  auto products = [&](int xa, int xb, auto&& one) {
-    bool acc = false;
-    for (int s = 2; s >= 0; --s)
-      for (int i = 0; i <= s; ++i) {
-        if (i >= xa || s - i >= xb) continue;
-        one(i, s - i, acc);
-        acc = true;
-      }
+  auto wait = [&](int bar, uint32_t phase) {
+    if (ok && !wait_phase(&sm.bar[bar], phase, kBudget)) ok = false;
+    return ok;
   };
+  auto chunk_row = [&](int ci) { return row0 + (REV ? nchunk - 1 - ci : ci) * kC; };
+  auto chunk_len = [&](int ci) { return min(kC, row0 + ntok - chunk_row(ci)); };
 
-  for (int ci = 0; ci < nchunk && ok; ++ci) {
-    const uint32_t ph = ci & 1;
-    const int64_t t0 = chunk_row(ci);
-    const int n = chunk_len(ci);
-    const int shift = ci == 0 && first ? r.shift : 0;
-    const int ksn = (n + 15) / 16;
-    const bool more = ci + 1 < nchunk;
-    tc::fence_before();
-    tc::fence_async_smem();
-    ok = __syncthreads_and(ok);  // operands of this chunk and the state are in place
-    if (!ok) break;
-    if (tid == 0) {
-      tc::fence_after();
+  if (warp == kWarps) {
+    const bool lead = tc::elect_one();
+    uint32_t open = 0, odd = 0;  // barriers with products in flight, and their phase
+    auto commit = [&](int bar, int ci) {
+      if (lead) tc::commit(&sm.bar[bar]);
+      open |= 1u << bar;
+      odd = (odd & ~(1u << bar)) | (uint32_t)(ci & 1) << bar;
+    };
+    // pairs of parts of a product with `xa` and `xb` parts, the largest last
+    auto products = [&](int xa, int xb, auto&& one) {
+      bool acc = false;
+#pragma unroll 1
+      for (int s = 2; s >= 0; --s)
+#pragma unroll 1
+        for (int i = 0; i <= s; ++i) {
+          if (i >= xa || s - i >= xb) continue;
+          one(i, s - i, acc);
+          acc = true;
+        }
+    };
+    const int ksq = (N + 15) / 16;
+    const uint32_t dK = kmajor(sK), dKt = mnmajor(sK), dV = mnmajor(sV), dX = mnmajor(sX), dS = mnmajor(sS);
+    for (int ci = 0; ci < nchunk; ++ci) {
+      const uint32_t ph = ci & 1;
+      const int ksn = (chunk_len(ci) + 15) / 16;
       if (!SUMMARY) {
-        const int ksq = (N + 15) / 16;
+        if (!wait(kBarQ, ph)) break;
+        tc::fence_after();
         products(IP, IP, [&](int i, int j, bool acc) {
-          for (int ks = 0; ks < ksq; ++ks)
-            mma_ts(tm + kColA, tm + kColQ + 64 * i, 8 * ks, kmajor(sK + j * kPartK), kstep(ks),
-                   idesc_bf16(128, kC, 0, 0), acc || ks > 0);
+#pragma unroll
+          for (int ks = 0; ks < NK / 16; ++ks)
+            if (ks < ksq && lead)
+              mma_ts(tm + kColA, tm + kColQ + 64 * i, 8 * ks, dK + j * (kPartK >> 4), kstep(ks),
+                     idesc_bf16(128, kC, 0, 0), acc || ks > 0);
         });
         products(IP, 3, [&](int i, int j, bool acc) {
-          for (int ks = 0; ks < ksq; ++ks)
-            mma_ts(tm + kColI, tm + kColQ + 64 * i, 8 * ks, mnmajor(sS + j * kPartS), mnstep(ks),
-                   idesc_bf16(128, 64, 0, 1), acc || ks > 0);
+#pragma unroll
+          for (int ks = 0; ks < NK / 16; ++ks)
+            if (ks < ksq && lead)
+              mma_ts(tm + kColI, tm + kColQ + 64 * i, 8 * ks, dS + j * (kPartS >> 4), mnstep(ks),
+                     idesc_bf16(128, 64, 0, 1), acc || ks > 0);
         });
-        tc::commit(barA);
-        pend[0] = ph;
+        commit(kBarA, ci);
       }
+      if (!wait(kBarX, ph)) break;
+      tc::fence_after();
       products(IP, 3, [&](int i, int j, bool acc) {
-        for (int ks = 0; ks < ksn; ++ks)
-          mma_ss(tm + kColS, mnmajor(sK + i * kPartK), mnstep(ks), mnmajor(sX + j * kPartV), mnstep(ks),
-                 idesc_bf16(NK, 64, 1, 1), acc || ks > 0);
+#pragma unroll
+        for (int ks = 0; ks < kC / 16; ++ks)
+          if (ks < ksn && lead)
+            mma_ss(tm + kColS, dKt + i * (kPartK >> 4), mnstep(ks), dX + j * (kPartV >> 4), mnstep(ks),
+                   idesc_bf16(NK, 64, 1, 1), acc || ks > 0);
       });
-      tc::commit(barB);
-      pend[1] = ph;
+      commit(kBarB, ci);
+      if (!SUMMARY) {
+        if (!wait(kBarP, ph)) break;
+        tc::fence_after();
+        products(3, IP, [&](int i, int j, bool acc) {
+#pragma unroll
+          for (int ks = 0; ks < kC / 16; ++ks)
+            if (ks < ksn && lead)
+              mma_ts(tm + kColO, tm + kColQ + 64 * i, 8 * ks, dV + j * (kPartV >> 4), mnstep(ks),
+                     idesc_bf16(128, 64, 0, 1), acc || ks > 0);
+        });
+        commit(kBarC, ci);
+      }
+    }
+    if (!ok) {  // bounded waits for what may still be in flight
+      if (lead) atomicExch(a.status, kStatusTimeout);
+      for (int i = 0; i < kBars; ++i)
+        if ((open >> i & 1) && !wait_phase(&sm.bar[i], odd >> i & 1, kBudget) && lead)
+          atomicExch(a.status, kStatusUndrained);
     }
     __syncwarp();
-    if (more) {
-      load_k(ci + 1);
-      load_v(ci + 1);
-      if (!SUMMARY) load_q(ci + 1);
-    }
-    if (!SUMMARY) {
-      ok = wait_phase(barA, ph, kBudget) && ok;
-      tc::fence_after();
-      // P: row i of this thread, 16-column blocks grp and grp + 4, into Q's columns
-      const int i = 32 * quad + lane;
+  } else {
+    auto arrive = [&](int bar) {
+      __syncwarp();
+      if (lane == 0) tc::bar_arrive(&sm.bar[bar]);
+    };
+    const T* gq = (const T*)r.q + (int64_t)(h / r.q_rep) * N;
+    const T* gk = (const T*)r.k + (int64_t)(h / r.k_rep) * N;
+    const T* gv = (const T*)r.v + (int64_t)(h / r.v_rep) * P;
+    const bool qvec = vec_rows<T>(gq, N, r.qs), kvec = vec_rows<T>(gk, N, r.ks), vvec = vec_rows<T>(gv, P, r.vs);
+    float4 rk[KQ], rv[VQ], rq[NB * 4];  // this thread's values of the next chunk
+    auto load_k = [&](int ci) {
+      const T* g = gk + (int64_t)chunk_row(ci) * r.ks;
+      const int n = chunk_len(ci);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int jb = grp + 4 * x, j0 = 16 * jb;
-        if (jb >= kC / 16) continue;
-        uint32_t pc[3][8] = {};
-        if (!(r.reverse ? j0 + 15 < 32 * quad : j0 > 32 * quad + 31)) {
-          float s[16];
-          ld16(tw + kColA + j0, s);
-          tc::tmem_wait_ld();
-          if (r.reverse ? j0 >= 32 * quad + 31 : j0 + 15 <= 32 * quad) {
-            const float f = r.intra * sm.pw[r.reverse ? j0 - i : i - j0 - 15];
+      for (int x = 0; x < KQ; ++x) {
+        const int t = tid / (NK / 4) + x * (32 * kWarps / (NK / 4)), c = tid % (NK / 4) * 4;
+        rk[x] = t < n ? load4<T>(g + t * r.ks, c, N, kvec) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    auto load_v = [&](int ci) {
+      const T* g = gv + (int64_t)chunk_row(ci) * r.vs;
+      const int n = chunk_len(ci);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s[e] *= f * sm.col[e];
-          } else {
+      for (int x = 0; x < VQ; ++x) {
+        const int t = tid / 16 + x * 2 * kWarps, c = p_lo + tid % 16 * 4;
+        rv[x] = t < n ? load4<T>(g + t * r.vs, c, P, vvec) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    // queries: tensor-memory row 32 quad + lane, columns NB * 16 grp ..
+    auto load_q = [&](int ci) {
+      const int t = 32 * quad + lane;
+      const T* g = gq + (int64_t)(chunk_row(ci) + t) * r.qs;
+      const bool in = t < chunk_len(ci);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int d = r.reverse ? j0 + e - i : i - j0 - e;
-              s[e] = d >= 0 ? s[e] * (r.intra * sm.pw[d < 0 ? 0 : d]) : 0.f;
-            }
-          }
+      for (int x = 0; x < NB * 4; ++x)
+        rq[x] = in ? load4<T>(g, NB * 16 * grp + 4 * x, N, qvec) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    // the next chunk's rows into L2, a 128-byte line a thread
+    auto prefetch = [&](int ci) {
+      const int n = chunk_len(ci);
+      auto lines = [&](const T* g, int64_t stride, int width) {
+        const int per = (width * (int)sizeof(T) + 127) / 128;
+        for (int x = tid; x < n * per; x += 32 * kWarps) {
+          const int t = x / per;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)(g + (int64_t)(chunk_row(ci) + t) * stride) +
+                                                        (x - t * per) * 128));
+        }
+      };
+      if (!SUMMARY) lines(gq, r.qs, N);
+      lines(gk, r.ks, N);
+      lines(gv + p_lo, r.vs, min(64, P - p_lo));
+    };
+    // A thread's quads of a tile lie a multiple of eight rows apart, so their places
+    // differ by constants.
+    auto put2 = [](char* at, uint32_t lo, uint32_t hi) { *reinterpret_cast<uint2*>(at) = make_uint2(lo, hi); };
+    constexpr int kRowsK = 32 * kWarps / (NK / 4), kRowsV = 32 * kWarps / 16;
+    static_assert(kRowsK % 8 == 0 && kRowsV % 8 == 0, "");
+    char* const at_k = raw + quad_at(tid / (NK / 4), tid % (NK / 4) * 4);
+    char* const at_v = raw + kParts * kPartK + quad_at(tid / 16, tid % 16 * 4);
+    auto put_k = [&]() {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint32_t t3[3];
-            cut2(s[2 * e], s[2 * e + 1], t3);
-            pc[0][e] = t3[0];
-            pc[1][e] = t3[1];
-            pc[2][e] = t3[2];
-          }
+      for (int x = 0; x < KQ; ++x) {
+        if (tid / (NK / 4) + x * kRowsK >= kC) continue;
+        uint32_t lo[3], hi[3];
+        cut2(rk[x].x, rk[x].y, lo);
+        cut2(rk[x].z, rk[x].w, hi);
+#pragma unroll
+        for (int p = 0; p < IP; ++p) put2(at_k + p * kPartK + x * kRowsK * 128, lo[p], hi[p]);
+      }
+    };
+    auto put_v = [&](int n) {  // V and V^
+#pragma unroll
+      for (int x = 0; x < VQ; ++x) {
+        const int t = tid / 16 + x * kRowsV;
+        if (t >= kC) continue;
+        uint32_t lo[3], hi[3];
+        if (!SUMMARY) {
+          cut2(rv[x].x, rv[x].y, lo);
+          cut2(rv[x].z, rv[x].w, hi);
+#pragma unroll
+          for (int p = 0; p < IP; ++p) put2(at_v + p * kPartV + x * kRowsV * 128, lo[p], hi[p]);
+        }
+        const float w = t < n ? r.kv * sm.pw[REV ? t : n - 1 - t] : 0.f;
+        cut2(w * rv[x].x, w * rv[x].y, lo);
+        cut2(w * rv[x].z, w * rv[x].w, hi);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) put2(at_v + (kParts + p) * kPartV + x * kRowsV * 128, lo[p], hi[p]);
+      }
+    };
+    auto put_q = [&]() {
+#pragma unroll
+      for (int y = 0; y < NB; ++y) {
+        uint32_t pc[8][3];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          cut2(rq[4 * y + x].x, rq[4 * y + x].y, pc[2 * x]);
+          cut2(rq[4 * y + x].z, rq[4 * y + x].w, pc[2 * x + 1]);
         }
 #pragma unroll
-        for (int p = 0; p < 3; ++p) st8(tw + kColQ + 64 * p + 8 * jb, pc[p]);
+        for (int p = 0; p < IP; ++p) {
+          uint32_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = pc[e][p];
+          st8(tw + kColQ + 64 * p + NB * 8 * grp + 8 * y, v);
+        }
       }
       tc::tmem_wait_st();
-      tc::fence_before();
-      ok = __syncthreads_and(ok);
-      if (!ok) break;
-      if (tid == 0) {
-        pend[0] = -1;
-        tc::fence_after();
-        products(3, IP, [&](int x, int y, bool acc) {
-          for (int ks = 0; ks < ksn; ++ks)
-            mma_ts(tm + kColO, tm + kColQ + 64 * x, 8 * ks, mnmajor(sV + y * kPartV), mnstep(ks),
-                   idesc_bf16(128, 64, 0, 1), acc || ks > 0);
-        });
-        tc::commit(barC);
-        pend[2] = ph;
-      }
-      __syncwarp();
-    }
-    ok = wait_phase(barB, ph, kBudget) && ok;
-    tc::fence_after();
-    {
-      const float dec = sm.pw[n - shift];
-      float kv[SC];
-      if constexpr (NB == 2) ld16(tw + kColS + scol, kv);
-      else ld_m64_8(tw + kColS + 16 * grp, kv);
-      tc::tmem_wait_ld();
-#pragma unroll
-      for (int j = 0; j < SC; ++j) st[j] = fmaf(dec, st[j], kv[j]);
-      if (!SUMMARY) put_state();
-    }
-    if (more) put_k();
-    if (SUMMARY) {
-      if (more) put_v(chunk_len(ci + 1));
-      continue;
-    }
-    ok = wait_phase(barC, ph, kBudget) && ok;
-    tc::fence_after();
-    if (more) {
-      put_v(chunk_len(ci + 1));
-      put_q();
-    }
-    {
-      const int i = 32 * quad + lane, at = min(max(r.reverse ? n - 1 - i : i, 0), kC - 1);
-      const float f = r.inter * sm.pw[at + 1 - shift];
-      const int c0 = 16 * grp;
-      float o[16], in[16];
-      ld16(tw + kColO + c0, o);
-      ld16(tw + kColI + c0, in);
-      tc::tmem_wait_ld();
-      if (i < n) {
-        const int64_t at_out = (row0 + t0 + i) * r.os + (int64_t)h * P + p_lo + c0;
-        float* of = (float*)r.out + at_out;
-        T* ot = (T*)r.out + at_out;
-        const bool f32 = r.out_rep > 1 || sizeof(T) == 4;
-        const bool vec = f32 && P % 4 == 0 && r.os % 4 == 0 && (reinterpret_cast<uintptr_t>(r.out) & 15) == 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = fmaf(f, in[e], o[e]);
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-          if (vec) {
-            if (p_lo + c0 + e < P) *(float4*)(of + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            continue;
-          }
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if (p_lo + c0 + e + y >= P) continue;
-            if (f32) of[e + y] = o[e + y];
-            else ot[e + y] = from_f32<T>(o[e + y]);
-          }
-        }
-      }
-    }
-  }
-
-  if (tid == 0 && !ok) {
-    atomicExch(a.status, kStatusTimeout);
-    for (int i = 0; i < 3; ++i)
-      if (pend[i] >= 0 && !wait_phase(&sm.bar[i], pend[i], kBudget)) atomicExch(a.status, kStatusUndrained);
-  }
-  if (ok && (SUMMARY || (r.fin && last))) {
-    const float f = !SUMMARY && len > 0 && r.fin_shift ? sm.pw[1] : 1.f;
+    };
+    const int srow = NB == 2 ? 32 * quad + lane : 16 * quad + (lane & 15);
+    const int scol = NB == 2 ? 16 * grp : 16 * grp + 8 * (lane >> 4);
+    float st[SC];
+    float* entry = a.entry ? a.entry + ri * a.entry_role +
+                                 ((int64_t)seg * a.B * a.H + bh) * ((int64_t)N * P)
+                           : nullptr;
+    const int64_t sbase = (int64_t)bh * N * P;
 #pragma unroll
     for (int j = 0; j < SC; ++j) {
       const int p = p_lo + scol + j;
-      if (srow < N && p < P) {
-        if (SUMMARY) entry[(int64_t)p * N + srow] = st[j];
-        else r.fin[sbase + (int64_t)p * r.sp + (int64_t)srow * r.sn] = f * st[j];
+      st[j] = 0.f;
+      if (!SUMMARY && srow < N && p < P) {
+        if (a.nseg > 1) st[j] = entry[(int64_t)p * N + srow];
+        else if (r.init) st[j] = r.init[sbase + (int64_t)p * r.sp + (int64_t)srow * r.sn];
       }
     }
+    auto put_state = [&]() {
+#pragma unroll
+      for (int c = 0; c < SC / 8; ++c) {
+        uint32_t pc[4][3];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cut2(st[8 * c + 2 * j], st[8 * c + 2 * j + 1], pc[j]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+          sts(sS + p * kPartS + chunk_at(srow, scol / 8 + c), make_uint4(pc[0][p], pc[1][p], pc[2][p], pc[3][p]));
+      }
+    };
+    const int i = 32 * quad + lane;  // this thread's row of A, P and O
+    // row factors of this warp's blocks of 16 columns before the diagonal
+    float fac[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int d = REV ? 16 * (grp + 4 * x) - i : i - 16 * (grp + 4 * x) - 15;
+      fac[x] = d < 0 ? 0.f : r.intra * sm.pw[d];
+    }
+    if (nchunk > 0) {
+      load_k(0);
+      load_v(0);
+      if (!SUMMARY) load_q(0);
+      put_k();
+      if (!SUMMARY) {
+        put_state();
+        put_q();
+        tc::fence_before();
+        tc::fence_async_smem();
+        arrive(kBarQ);
+      }
+      put_v(chunk_len(0));
+      tc::fence_async_smem();
+      arrive(kBarX);
+    }
+    for (int ci = 0; ci < nchunk; ++ci) {
+      const uint32_t ph = ci & 1;
+      const int n = chunk_len(ci);
+      const int shift = ci == 0 && first ? r.shift : 0;
+      const bool more = ci + 1 < nchunk;
+      if (more) prefetch(ci + 1);
+      if (!SUMMARY) {
+        if (!wait(kBarA, ph)) break;
+        tc::fence_after();
+        // P: 16-column blocks grp and grp + 4, into Q's columns
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int jb = grp + 4 * x, j0 = 16 * jb;
+          if (jb >= kC / 16) continue;
+          uint32_t pc[3][8] = {};
+          if (REV ? j0 + 15 >= 32 * quad : j0 <= 32 * quad + 31) {
+            float s[16];
+            ld16(tw + kColA + j0, s);
+            tc::tmem_wait_ld();
+            if (REV ? j0 >= 32 * quad + 31 : j0 + 15 <= 32 * quad) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(&sm.col[e]);
+                s[e] *= fac[x] * w.x;
+                s[e + 1] *= fac[x] * w.y;
+                s[e + 2] *= fac[x] * w.z;
+                s[e + 3] *= fac[x] * w.w;
+              }
+            } else {
+              int d0 = REV ? j0 - i : i - j0;
+              asm volatile("" : "+r"(d0));  // not worth sixteen registers between chunks
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int d = REV ? d0 + e : d0 - e;
+                const float w = r.intra * sm.pw[max(d, 0)];
+                s[e] = d >= 0 ? s[e] * w : 0.f;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              uint32_t t3[3];
+              cut2(s[2 * e], s[2 * e + 1], t3);
+              pc[0][e] = t3[0];
+              pc[1][e] = t3[1];
+              pc[2][e] = t3[2];
+            }
+          }
+#pragma unroll
+          for (int p = 0; p < 3; ++p) st8(tw + kColQ + 64 * p + 8 * jb, pc[p]);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before();
+        arrive(kBarP);
+      }
+      if (more) load_k(ci + 1);
+      if (!wait(kBarB, ph)) break;
+      tc::fence_after();
+      {
+        const float dec = sm.pw[n - shift];
+        float kv[SC];
+        if constexpr (NB == 2) ld16(tw + kColS + scol, kv);
+        else ld_m64_8(tw + kColS + 16 * grp, kv);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < SC; ++j) st[j] = fmaf(dec, st[j], kv[j]);
+        if (!SUMMARY && more) put_state();
+      }
+      tc::fence_before();
+      if (more) put_k();
+      if (SUMMARY) {
+        if (more) {
+          load_v(ci + 1);
+          put_v(chunk_len(ci + 1));
+          tc::fence_async_smem();
+          arrive(kBarX);
+        }
+        continue;
+      }
+      if (more) load_q(ci + 1);
+      if (!wait(kBarC, ph)) break;
+      tc::fence_after();
+      {
+        const int at = min(max(REV ? n - 1 - i : i, 0), kC - 1);
+        const float f = r.inter * sm.pw[at + 1 - shift];
+        const bool f32 = r.out_rep > 1 || sizeof(T) == 4;
+        const bool vec = f32 && P % 4 == 0 && r.os % 4 == 0 && (reinterpret_cast<uintptr_t>(r.out) & 15) == 0;
+        const int64_t row = (int64_t)(chunk_row(ci) + i) * r.os + (int64_t)h * P + p_lo;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {  // eight columns at a time: the queries are in registers too
+          const int c0 = 16 * grp + 8 * x;
+          float o[8], in[8];
+          ld8(tw + kColO + c0, o);
+          ld8(tw + kColI + c0, in);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(f, in[e], o[e]);
+          if (i < n) {
+            float* of = (float*)r.out + row + c0;
+            T* ot = (T*)r.out + row + c0;
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+              if (vec) {
+                if (p_lo + c0 + e < P) *(float4*)(of + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                continue;
+              }
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                if (p_lo + c0 + e + y >= P) continue;
+                if (f32) of[e + y] = o[e + y];
+                else ot[e + y] = from_f32<T>(o[e + y]);
+              }
+            }
+          }
+        }
+      }
+      if (more) {
+        put_q();
+        tc::fence_before();
+        tc::fence_async_smem();
+        arrive(kBarQ);
+        // A and Oi, some 4,000 cycles, hide these loads
+        load_v(ci + 1);
+        put_v(chunk_len(ci + 1));
+        tc::fence_async_smem();
+        arrive(kBarX);
+      }
+    }
+    if (ok && (SUMMARY || (r.fin && last))) {
+      const float f = !SUMMARY && len > 0 && r.fin_shift ? sm.pw[1] : 1.f;
+#pragma unroll
+      for (int j = 0; j < SC; ++j) {
+        const int p = p_lo + scol + j;
+        if (srow < N && p < P) {
+          if (SUMMARY) entry[(int64_t)p * N + srow] = st[j];
+          else r.fin[sbase + (int64_t)p * r.sp + (int64_t)srow * r.sn] = f * st[j];
+        }
+      }
+    }
+    if (!ok && lane == 0) atomicExch(a.status, kStatusTimeout);
   }
   tc::fence_before();
   __syncthreads();
@@ -459,16 +544,25 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
 }
 
 template <typename T, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads, 1)
-    k_la_split(const __grid_constant__ LaArgs a, int items) {
+__global__ void __launch_bounds__(kThreads, 1) k_la_split(const __grid_constant__ LaArgs a) {
   extern __shared__ __align__(1024) char raw[];
   la_clear_status<SUMMARY>(a);
-  int item = blockIdx.x % items, ri = 0;
-  const int unit = blockIdx.x / items;
-  while (item >= (a.role[ri].P + 63) / 64) item -= (a.role[ri++].P + 63) / 64;
+  const int units = a.B * a.H * a.nseg;
+  int x = blockIdx.x, ri = 0, tiles = (a.role[0].P + 63) / 64;
+  while (x >= units * tiles) {
+    x -= units * tiles;
+    tiles = (a.role[++ri].P + 63) / 64;
+  }
+  const int item = x % tiles, unit = x / tiles;
   const int bh = unit % (a.B * a.H), seg = unit / (a.B * a.H);
-  if (a.role[ri].N > 64) walk<T, 2, SUMMARY>(a, ri, item, bh, seg, raw);
-  else walk<T, 1, SUMMARY>(a, ri, item, bh, seg, raw);
+  const LaRole& r = a.role[ri];
+  if (r.N > 64) {
+    if (r.reverse) walk<T, 2, SUMMARY, true>(a, ri, item, bh, seg, raw);
+    else walk<T, 2, SUMMARY, false>(a, ri, item, bh, seg, raw);
+  } else {
+    if (r.reverse) walk<T, 1, SUMMARY, true>(a, ri, item, bh, seg, raw);
+    else walk<T, 1, SUMMARY, false>(a, ri, item, bh, seg, raw);
+  }
 }
 
 }  // namespace
@@ -480,7 +574,7 @@ cudaError_t launch_la_split(const LaArgs& a, LaPass pass, cudaStream_t s) {
   auto go = [&](auto kernel) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, kSmem, s>>>(a, items);
+    kernel<<<grid, kThreads, kSmem, s>>>(a);
     count_launches(1);
     return cudaGetLastError();
   };

@@ -47,6 +47,14 @@ __device__ __forceinline__ void ld16(uint32_t addr, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void ld8(uint32_t addr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 // Rows of a 64-row accumulator (lanes 0..15 of each quarter): lanes 0..15 get the
 // eight columns at the address, lanes 16..31 the next eight. No wait.
 __device__ __forceinline__ void ld_m64_8(uint32_t addr, float* v) {
