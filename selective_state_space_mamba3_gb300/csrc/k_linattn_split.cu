@@ -120,7 +120,7 @@ __device__ __forceinline__ bool vec_rows(const void* p, int width, int64_t strid
 // One block's walk (see k_linattn_mma.cu: warps 0..15 compute, one lane of warp 16
 // issues the products, and they meet at mbarriers with bounded waits). NB:
 // 64-column blocks of N.
-template <typename T, int NB, bool SUMMARY, bool REV>
+template <typename T, int NB, bool SUMMARY>
 __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, int seg, char* raw) {
   constexpr int IP = sizeof(T) == 4 ? 3 : 1;  // parts of an input
   constexpr int NK = 64 * NB;
@@ -132,14 +132,15 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
   const int quad = warp & 3, grp = (warp >> 2) & 3;
   const int b = bh / a.H, h = bh - b * a.H;
   const int N = r.N, P = r.P, p_lo = 64 * pt;
+  const bool rev = r.reverse;
   int64_t seq0, len;
   la_rows(a, b, &seq0, &len);
   const int last_seg = len > 0 ? (int)((len - 1) / a.seg_len) : 0;
   if (seg > last_seg) return;
   const int row0 = (int)(seq0 + seg * a.seg_len);  // the segment's rows
   const int ntok = (int)min(len - seg * a.seg_len, a.seg_len);
-  if (SUMMARY && seg == (REV ? 0 : last_seg)) return;  // the prefix pass never reads it
-  const bool first = seg == (REV ? last_seg : 0), last = seg == (REV ? 0 : last_seg);
+  if (SUMMARY && seg == (rev ? 0 : last_seg)) return;  // the prefix pass never reads it
+  const bool first = seg == (rev ? last_seg : 0), last = seg == (rev ? 0 : last_seg);
   const int nchunk = (ntok + kC - 1) / kC;
 
   const uint32_t base = tc::smem_u32(raw);
@@ -153,7 +154,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
   }
   const float ld = a.log_decay[h];
   if (tid < kC + 20) sm.pw[tid] = la_power(ld, tid);
-  if (tid < 16) sm.col[tid] = la_power(ld, REV ? tid : 15 - tid);
+  if (tid < 16) sm.col[tid] = la_power(ld, rev ? tid : 15 - tid);
   if (warp == 0) tc::tmem_alloc(&sm.tmem, kCols);
   __syncthreads();
   const uint32_t tm = sm.tmem, tw = tm + ((uint32_t)(32 * quad) << 16);
@@ -162,7 +163,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
     if (ok && !wait_phase(&sm.bar[bar], phase, kBudget)) ok = false;
     return ok;
   };
-  auto chunk_row = [&](int ci) { return row0 + (REV ? nchunk - 1 - ci : ci) * kC; };
+  auto chunk_row = [&](int ci) { return row0 + (rev ? nchunk - 1 - ci : ci) * kC; };
   auto chunk_len = [&](int ci) { return min(kC, row0 + ntok - chunk_row(ci)); };
 
   if (warp == kWarps) {
@@ -248,7 +249,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
     const T* gk = (const T*)r.k + (int64_t)(h / r.k_rep) * N;
     const T* gv = (const T*)r.v + (int64_t)(h / r.v_rep) * P;
     const bool qvec = vec_rows<T>(gq, N, r.qs), kvec = vec_rows<T>(gk, N, r.ks), vvec = vec_rows<T>(gv, P, r.vs);
-    float4 rk[KQ], rv[VQ], rq[NB * 4];  // this thread's values of the next chunk
+    float4 rk[KQ], rv[VQ], rq[4];  // this thread's values of the next chunk
     auto load_k = [&](int ci) {
       const T* g = gk + (int64_t)chunk_row(ci) * r.ks;
       const int n = chunk_len(ci);
@@ -267,29 +268,46 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
         rv[x] = t < n ? load4<T>(g + t * r.vs, c, P, vvec) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     };
-    // queries: tensor-memory row 32 quad + lane, columns NB * 16 grp ..
-    auto load_q = [&](int ci) {
-      const int t = 32 * quad + lane;
-      const T* g = gq + (int64_t)(chunk_row(ci) + t) * r.qs;
-      const bool in = t < chunk_len(ci);
-#pragma unroll
-      for (int x = 0; x < NB * 4; ++x)
-        rq[x] = in ? load4<T>(g, NB * 16 * grp + 4 * x, N, qvec) : make_float4(0.f, 0.f, 0.f, 0.f);
-    };
-    // the next chunk's rows into L2, a 128-byte line a thread
-    auto prefetch = [&](int ci) {
+    // Queries: this warp's 32 rows, 16 columns (half y of its NB) at a time, four
+    // lanes a row; turn_q() leaves each lane with the columns of one row.
+    auto load_q = [&](int ci, int y) {
       const int n = chunk_len(ci);
-      auto lines = [&](const T* g, int64_t stride, int width) {
-        const int per = (width * (int)sizeof(T) + 127) / 128;
-        for (int x = tid; x < n * per; x += 32 * kWarps) {
-          const int t = x / per;
-          asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)(g + (int64_t)(chunk_row(ci) + t) * stride) +
-                                                        (x - t * per) * 128));
+      const T* g = gq + (int64_t)chunk_row(ci) * r.qs;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int t = 32 * quad + lane / 4 + 8 * x;
+        rq[x] = t < n ? load4<T>(g + t * r.qs, NB * 16 * grp + 16 * y + lane % 4 * 4, N, qvec)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    };
+    // Register x of lane (l / 4, c) holds quad c of row 8 x + l / 4. The register's
+    // index and the lane's low bits change places, a bit a step, and quad x of row i
+    // comes to lie in register x.
+    auto turn_q = [&]() {
+#pragma unroll
+      for (int bit = 1; bit < 4; bit *= 2) {
+        const bool up = lane & bit;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (x & bit) continue;
+          const float4 keep = up ? rq[x | bit] : rq[x];
+          float4 give = up ? rq[x] : rq[x | bit];
+          give.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+          give.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+          give.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+          give.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+          rq[x] = up ? give : keep;
+          rq[x | bit] = up ? keep : give;
         }
-      };
-      if (!SUMMARY) lines(gq, r.qs, N);
-      lines(gk, r.ks, N);
-      lines(gv + p_lo, r.vs, min(64, P - p_lo));
+      }
+    };
+    // Rows of a later chunk into L2, one a thread. With 217 KB of shared memory the
+    // L1 has room for some 28 KB of loads in flight, so their latency has to be L2's.
+    auto prefetch = [&](const T* g, int64_t stride, int width, int ci, int t) {
+      if (ci >= nchunk || t < 0 || t >= chunk_len(ci)) return;
+      const char* p = (const char*)(g + (int64_t)(chunk_row(ci) + t) * stride);
+      const uint32_t skip = (uint32_t)(16 - ((uintptr_t)p & 15)) & 15, bytes = width * (uint32_t)sizeof(T);
+      if (bytes > skip + 15) tc::prefetch_l2(p + skip, (bytes - skip) & ~15u);
     };
     // A thread's quads of a tile lie a multiple of eight rows apart, so their places
     // differ by constants.
@@ -321,31 +339,29 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
 #pragma unroll
           for (int p = 0; p < IP; ++p) put2(at_v + p * kPartV + x * kRowsV * 128, lo[p], hi[p]);
         }
-        const float w = t < n ? r.kv * sm.pw[REV ? t : n - 1 - t] : 0.f;
+        const float w = t < n ? r.kv * sm.pw[rev ? t : n - 1 - t] : 0.f;
         cut2(w * rv[x].x, w * rv[x].y, lo);
         cut2(w * rv[x].z, w * rv[x].w, hi);
 #pragma unroll
         for (int p = 0; p < 3; ++p) put2(at_v + (kParts + p) * kPartV + x * kRowsV * 128, lo[p], hi[p]);
       }
     };
-    auto put_q = [&]() {
+    auto put_q = [&](int y) {
+      turn_q();
+      uint32_t pc[3][8];
 #pragma unroll
-      for (int y = 0; y < NB; ++y) {
-        uint32_t pc[8][3];
+      for (int x = 0; x < 4; ++x) {
+        uint32_t lo[3], hi[3];
+        cut2(rq[x].x, rq[x].y, lo);
+        cut2(rq[x].z, rq[x].w, hi);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          cut2(rq[4 * y + x].x, rq[4 * y + x].y, pc[2 * x]);
-          cut2(rq[4 * y + x].z, rq[4 * y + x].w, pc[2 * x + 1]);
-        }
-#pragma unroll
-        for (int p = 0; p < IP; ++p) {
-          uint32_t v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = pc[e][p];
-          st8(tw + kColQ + 64 * p + NB * 8 * grp + 8 * y, v);
+        for (int p = 0; p < 3; ++p) {
+          pc[p][2 * x] = lo[p];
+          pc[p][2 * x + 1] = hi[p];
         }
       }
-      tc::tmem_wait_st();
+#pragma unroll
+      for (int p = 0; p < IP; ++p) st8(tw + kColQ + 64 * p + NB * 8 * grp + 8 * y, pc[p]);
     };
     const int srow = NB == 2 ? 32 * quad + lane : 16 * quad + (lane & 15);
     const int scol = NB == 2 ? 16 * grp : 16 * grp + 8 * (lane >> 4);
@@ -374,22 +390,27 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
           sts(sS + p * kPartS + chunk_at(srow, scol / 8 + c), make_uint4(pc[0][p], pc[1][p], pc[2][p], pc[3][p]));
       }
     };
-    const int i = 32 * quad + lane;  // this thread's row of A, P and O
+    // this thread's row of A, P and O: the token that its tensor-memory row holds
+    const int i = 32 * quad + lane % 4 * 8 + lane / 4;
     // row factors of this warp's blocks of 16 columns before the diagonal
     float fac[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int d = REV ? 16 * (grp + 4 * x) - i : i - 16 * (grp + 4 * x) - 15;
+      const int d = rev ? 16 * (grp + 4 * x) - i : i - 16 * (grp + 4 * x) - 15;
       fac[x] = d < 0 ? 0.f : r.intra * sm.pw[d];
     }
     if (nchunk > 0) {
       load_k(0);
       load_v(0);
-      if (!SUMMARY) load_q(0);
       put_k();
       if (!SUMMARY) {
         put_state();
-        put_q();
+#pragma unroll
+        for (int y = 0; y < NB; ++y) {
+          load_q(0, y);
+          put_q(y);
+        }
+        tc::tmem_wait_st();
         tc::fence_before();
         tc::fence_async_smem();
         arrive(kBarQ);
@@ -403,7 +424,9 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
       const int n = chunk_len(ci);
       const int shift = ci == 0 && first ? r.shift : 0;
       const bool more = ci + 1 < nchunk;
-      if (more) prefetch(ci + 1);
+      prefetch(gk, r.ks, N, ci + 1, tid);
+      prefetch(gv + p_lo, r.vs, min(64, P - p_lo), ci + 1, tid - kC);
+      if (!SUMMARY) prefetch(gq, r.qs, N, ci + 1, tid - 2 * kC);
       if (!SUMMARY) {
         if (!wait(kBarA, ph)) break;
         tc::fence_after();
@@ -412,47 +435,50 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
         for (int x = 0; x < 2; ++x) {
           const int jb = grp + 4 * x, j0 = 16 * jb;
           if (jb >= kC / 16) continue;
-          uint32_t pc[3][8] = {};
-          if (REV ? j0 + 15 >= 32 * quad : j0 <= 32 * quad + 31) {
-            float s[16];
-            ld16(tw + kColA + j0, s);
-            tc::tmem_wait_ld();
-            if (REV ? j0 >= 32 * quad + 31 : j0 + 15 <= 32 * quad) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4) {
-                const float4 w = *reinterpret_cast<const float4*>(&sm.col[e]);
-                s[e] *= fac[x] * w.x;
-                s[e + 1] *= fac[x] * w.y;
-                s[e + 2] *= fac[x] * w.z;
-                s[e + 3] *= fac[x] * w.w;
+          for (int y = 0; y < 2; ++y) {
+            uint32_t pc[3][4] = {};
+            if (rev ? j0 + 15 >= 32 * quad : j0 <= 32 * quad + 31) {
+              float s[8];
+              ld8(tw + kColA + j0 + 8 * y, s);
+              tc::tmem_wait_ld();
+              if (rev ? j0 >= 32 * quad + 31 : j0 + 15 <= 32 * quad) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                  const float4 w = *reinterpret_cast<const float4*>(&sm.col[8 * y + e]);
+                  s[e] *= fac[x] * w.x;
+                  s[e + 1] *= fac[x] * w.y;
+                  s[e + 2] *= fac[x] * w.z;
+                  s[e + 3] *= fac[x] * w.w;
+                }
+              } else {
+                int d0 = rev ? j0 + 8 * y - i : i - j0 - 8 * y;
+                const int step = rev ? 1 : -1;
+                asm volatile("" : "+r"(d0));  // not worth registers between chunks
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int d = d0 + step * e;
+                  const float w = r.intra * sm.pw[max(d, 0)];
+                  s[e] = d >= 0 ? s[e] * w : 0.f;
+                }
               }
-            } else {
-              int d0 = REV ? j0 - i : i - j0;
-              asm volatile("" : "+r"(d0));  // not worth sixteen registers between chunks
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int d = REV ? d0 + e : d0 - e;
-                const float w = r.intra * sm.pw[max(d, 0)];
-                s[e] = d >= 0 ? s[e] * w : 0.f;
+              for (int e = 0; e < 4; ++e) {
+                uint32_t t3[3];
+                cut2(s[2 * e], s[2 * e + 1], t3);
+                pc[0][e] = t3[0];
+                pc[1][e] = t3[1];
+                pc[2][e] = t3[2];
               }
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              uint32_t t3[3];
-              cut2(s[2 * e], s[2 * e + 1], t3);
-              pc[0][e] = t3[0];
-              pc[1][e] = t3[1];
-              pc[2][e] = t3[2];
-            }
+            for (int p = 0; p < 3; ++p) st4(tw + kColQ + 64 * p + 8 * jb + 4 * y, pc[p]);
           }
-#pragma unroll
-          for (int p = 0; p < 3; ++p) st8(tw + kColQ + 64 * p + 8 * jb, pc[p]);
         }
         tc::tmem_wait_st();
         tc::fence_before();
         arrive(kBarP);
       }
-      if (more) load_k(ci + 1);
       if (!wait(kBarB, ph)) break;
       tc::fence_after();
       {
@@ -466,7 +492,10 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
         if (!SUMMARY && more) put_state();
       }
       tc::fence_before();
-      if (more) put_k();
+      if (more) {
+        load_k(ci + 1);
+        put_k();
+      }
       if (SUMMARY) {
         if (more) {
           load_v(ci + 1);
@@ -476,15 +505,18 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
         }
         continue;
       }
-      if (more) load_q(ci + 1);
+      if (more) load_q(ci + 1, 0);
       if (!wait(kBarC, ph)) break;
       tc::fence_after();
       {
-        const int at = min(max(REV ? n - 1 - i : i, 0), kC - 1);
+        const int at = min(max(rev ? n - 1 - i : i, 0), kC - 1);
         const float f = r.inter * sm.pw[at + 1 - shift];
         const bool f32 = r.out_rep > 1 || sizeof(T) == 4;
         const bool vec = f32 && P % 4 == 0 && r.os % 4 == 0 && (reinterpret_cast<uintptr_t>(r.out) & 15) == 0;
-        const int64_t row = (int64_t)(chunk_row(ci) + i) * r.os + (int64_t)h * P + p_lo;
+        const int64_t base_out = (int64_t)chunk_row(ci) * r.os + (int64_t)h * P + p_lo;
+        // rows of lanes l < 16 and l + 16
+        constexpr int kHalf = 4;
+        const int i_lo = i - (lane & 16 ? kHalf : 0);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {  // eight columns at a time: the queries are in registers too
           const int c0 = 16 * grp + 8 * x;
@@ -494,27 +526,43 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
           tc::tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 8; ++e) o[e] = fmaf(f, in[e], o[e]);
-          if (i < n) {
-            float* of = (float*)r.out + row + c0;
-            T* ot = (T*)r.out + row + c0;
+          if (vec) {
+            // lanes l and l ^ 16 exchange halves: each writes four columns of both
+            // rows, so that a row's 32 bytes leave in one store
+            const bool up = lane & 16;
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-              if (vec) {
-                if (p_lo + c0 + e < P) *(float4*)(of + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                continue;
-              }
+            for (int e = 0; e < 4; ++e) {
+              const float give = __shfl_xor_sync(0xffffffffu, up ? o[e] : o[4 + e], 16);
+              const float keep = up ? o[4 + e] : o[e];
+              o[e] = up ? give : keep;
+              o[4 + e] = up ? keep : give;
+            }
+            // o[0..3]: the lower lane's row, o[4..7]: the upper lane's
+            float* of = (float*)r.out + base_out + c0 + (up ? 4 : 0);
+            const int lo = i_lo, hi = i_lo + kHalf;
+            if (p_lo + c0 + (up ? 4 : 0) < P) {
+              if (lo < n) *(float4*)(of + lo * r.os) = make_float4(o[0], o[1], o[2], o[3]);
+              if (hi < n) *(float4*)(of + hi * r.os) = make_float4(o[4], o[5], o[6], o[7]);
+            }
+          } else if (i < n) {
+            float* of = (float*)r.out + base_out + i * r.os + c0;
+            T* ot = (T*)r.out + base_out + i * r.os + c0;
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                if (p_lo + c0 + e + y >= P) continue;
-                if (f32) of[e + y] = o[e + y];
-                else ot[e + y] = from_f32<T>(o[e + y]);
-              }
+            for (int e = 0; e < 8; ++e) {
+              if (p_lo + c0 + e >= P) continue;
+              if (f32) of[e] = o[e];
+              else ot[e] = from_f32<T>(o[e]);
             }
           }
         }
       }
       if (more) {
-        put_q();
+#pragma unroll
+        for (int y = 0; y < NB; ++y) {
+          put_q(y);
+          if (y + 1 < NB) load_q(ci + 1, y + 1);
+        }
+        tc::tmem_wait_st();
         tc::fence_before();
         tc::fence_async_smem();
         arrive(kBarQ);
@@ -556,13 +604,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_la_split(const __grid_constant_
   const int item = x % tiles, unit = x / tiles;
   const int bh = unit % (a.B * a.H), seg = unit / (a.B * a.H);
   const LaRole& r = a.role[ri];
-  if (r.N > 64) {
-    if (r.reverse) walk<T, 2, SUMMARY, true>(a, ri, item, bh, seg, raw);
-    else walk<T, 2, SUMMARY, false>(a, ri, item, bh, seg, raw);
-  } else {
-    if (r.reverse) walk<T, 1, SUMMARY, true>(a, ri, item, bh, seg, raw);
-    else walk<T, 1, SUMMARY, false>(a, ri, item, bh, seg, raw);
-  }
+  if (r.N > 64) walk<T, 2, SUMMARY>(a, ri, item, bh, seg, raw);
+  else walk<T, 1, SUMMARY>(a, ri, item, bh, seg, raw);
 }
 
 }  // namespace
