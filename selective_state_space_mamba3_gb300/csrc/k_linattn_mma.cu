@@ -120,7 +120,7 @@ __device__ __forceinline__ void tma_store_wait_read() {
 // They meet at mbarriers only (one phase a chunk each, arrivals one a warp), and
 // every wait is bounded, so a thread whose wait gives up leaves the loop and the
 // others follow as theirs do.
-template <int NB, bool SUMMARY, bool REV, bool MILD>
+template <int NB, bool SUMMARY, bool MILD>
 __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, int pt, int bh,
                                      int seg, char* raw) {
   constexpr int NK = 64 * NB;
@@ -129,14 +129,15 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = bh / a.H, h = bh - b * a.H;
   const int N = r.N, P = r.P, p_lo = 64 * pt;
+  const bool rev = r.reverse;
   int64_t seq0, len;
   la_rows(a, b, &seq0, &len);
   const int last_seg = len > 0 ? (int)((len - 1) / a.seg_len) : 0;
   if (seg > last_seg) return;
   const int row0 = (int)(seq0 + seg * a.seg_len);                        // the segment's rows
   const int ntok = (int)min(len - seg * a.seg_len, a.seg_len);
-  if (SUMMARY && seg == (REV ? 0 : last_seg)) return;  // the prefix pass never reads it
-  const bool first = seg == (REV ? last_seg : 0), last = seg == (REV ? 0 : last_seg);
+  if (SUMMARY && seg == (rev ? 0 : last_seg)) return;  // the prefix pass never reads it
+  const bool first = seg == (rev ? last_seg : 0), last = seg == (rev ? 0 : last_seg);
   const int nchunk = (ntok + kC - 1) / kC;
 
   const uint32_t base = tc::smem_u32(raw);
@@ -150,8 +151,8 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
   const float ld = a.log_decay[h];
   if (tid <= kC / 2) sm.pw[tid] = la_power(ld, tid);
   if (tid < kC) {
-    if (MILD) sm.col[tid] = expf(ld * (float)(REV ? tid - kC / 2 : kC / 2 - tid));
-    else if (tid < 16) sm.col[tid] = la_power(ld, REV ? tid : 15 - tid);
+    if (MILD) sm.col[tid] = expf(ld * (float)(rev ? tid - kC / 2 : kC / 2 - tid));
+    else if (tid < 16) sm.col[tid] = la_power(ld, rev ? tid : 15 - tid);
   }
   auto power = [&](int d) { return d <= kC / 2 ? sm.pw[d] : sm.pw[kC / 2] * sm.pw[d - kC / 2]; };
   if (warp == 0) tc::tmem_alloc(&sm.tmem, kCols);
@@ -191,7 +192,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
     }
     if (!SUMMARY)
       put_state(ratio * (!MILD ? 1.f
-                         : !REV ? la_power(ld, kC / 2 + 1)
+                         : !rev ? la_power(ld, kC / 2 + 1)
                                 : expf(ld * (float)(min(kC, ntok - (nchunk - 1) * kC) - (first ? r.shift : 0) - kC / 2))));
   }
   tc::fence_async_smem();
@@ -202,7 +203,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
     if (ok && !wait_phase(&sm.bar[bar], phase, kBudget)) ok = false;
     return ok;
   };
-  auto chunk_row = [&](int ci) { return row0 + (REV ? nchunk - 1 - ci : ci) * kC; };
+  auto chunk_row = [&](int ci) { return row0 + (rev ? nchunk - 1 - ci : ci) * kC; };
   auto chunk_len = [&](int ci) { return min(kC, row0 + ntok - chunk_row(ci)); };
 
   if (warp == kWarps && nchunk > 0) {
@@ -339,11 +340,11 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
     // is the output's. Stronger decays take a row factor for every block of 16
     // columns, and lam^d from the table on the diagonal.
     const float intra = r.intra;
-    const float rowf = MILD ? intra * expf(ld * (float)(REV ? kC / 2 - i : i - kC / 2)) : 1.f;
+    const float rowf = MILD ? intra * expf(ld * (float)(rev ? kC / 2 - i : i - kC / 2)) : 1.f;
     float fac[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      const int c = 32 * grp + 16 * x, d = REV ? c - i : i - c - 15;
+      const int c = 32 * grp + 16 * x, d = rev ? c - i : i - c - 15;
       fac[x] = MILD || d < 0 ? 0.f : intra * power(d);
     }
     for (int ci = 0; ci < nchunk; ++ci) {
@@ -365,7 +366,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
       if (!wait(kBarV, ph)) break;
       {
         const int j = tid >> 2;
-        const float w = j < n ? r.kv * power(REV ? j : n - 1 - j) : 0.f;
+        const float w = j < n ? r.kv * power(rev ? j : n - 1 - j) : 0.f;
         uint4 low[2];
         if (!SUMMARY && ci > 0 && !wait(kBarX, ph ^ 1)) break;  // the last output has left X
 #pragma unroll
@@ -413,11 +414,11 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
         for (int x = 0; x < 2; ++x) {
           const int c = 32 * grp + 16 * x;
           uint32_t pk[8] = {};
-          if (REV ? c + 15 >= 32 * quad : c <= 32 * quad + 31) {
+          if (rev ? c + 15 >= 32 * quad : c <= 32 * quad + 31) {
             float s[16];
             ld16(tw + c, s);
             tc::tmem_wait_ld();
-            const bool full = REV ? c >= 32 * quad + 32 : c < 32 * quad;
+            const bool full = rev ? c >= 32 * quad + 32 : c < 32 * quad;
             if (MILD || full) {
               const float2 f2 = make_float2(fac[x], fac[x]);
 #pragma unroll
@@ -436,11 +437,12 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
               }
             }
             if (!full) {
-              int d0 = REV ? c - i : i - c;
+              int d0 = rev ? c - i : i - c;
+              const int step = rev ? 1 : -1;
               asm volatile("" : "+r"(d0));  // sixteen addresses and tests are not worth registers between chunks
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const int d = REV ? d0 + e : d0 - e;
+                const int d = d0 + step * e;
                 if (!MILD) s[e] *= intra * power(max(d, 0));
                 s[e] = d >= 0 ? s[e] : 0.f;
               }
@@ -451,7 +453,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
           st8(tw + 32 * grp + 8 * x, pk);
         }
         if (!MILD) {  // Oi scaled in place, for O to be added
-          const int at = max(REV ? n - 1 - i : i, 0);
+          const int at = max(rev ? n - 1 - i : i, 0);
           const float f = r.inter * power(at + 1 - shift);
           float o[16];
           ld16(tw + kColO + 16 * grp, o);
@@ -477,7 +479,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
         tc::tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < SC; ++j) st[j] = fmaf(dec, st[j], kv[j]);
-        if (!SUMMARY) put_state(ratio * power(REV ? kC / 2 : kC / 2 + 1));
+        if (!SUMMARY) put_state(ratio * power(rev ? kC / 2 : kC / 2 + 1));
       }
       tc::fence_before();
       tc::fence_async_smem();
@@ -555,16 +557,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   const LaRole& r = a.role[ri];
   const float ld = a.log_decay[bh % a.H], ratio = r.inter / r.intra;
   const bool mild = fabsf(ld) <= 1.f && fabsf(ratio) < 1e6f && fabsf(ratio) > 1e-6f;  // else: strong, or scale 0
-  auto go = [&](auto nb, auto rev) {
-    if (mild && !SUMMARY) walk<nb.value, SUMMARY, rev.value, true>(a, maps, ri, item, bh, seg, raw);
-    else walk<nb.value, SUMMARY, rev.value, false>(a, maps, ri, item, bh, seg, raw);
+  auto go = [&](auto nb) {
+    if (mild && !SUMMARY) walk<nb.value, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
+    else walk<nb.value, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);
   };
-  auto by_way = [&](auto nb) {
-    if (r.reverse) go(nb, std::true_type());
-    else go(nb, std::false_type());
-  };
-  if (r.N > 64) by_way(std::integral_constant<int, 2>());
-  else by_way(std::integral_constant<int, 1>());
+  if (r.N > 64) go(std::integral_constant<int, 2>());
+  else go(std::integral_constant<int, 1>());
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
