@@ -545,7 +545,7 @@ template <bool SUMMARY>
 __global__ void __launch_bounds__(kThreads, 2)
     k_la_mma(const __grid_constant__ LaArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) char raw[];
-  la_clear_status<SUMMARY>(a);
+  la_clear_status(a);
   const int units = a.B * a.H * a.nseg;
   int x = blockIdx.x, ri = 0, tiles = (a.role[0].P + 63) / 64;
   while (x >= units * tiles) {
