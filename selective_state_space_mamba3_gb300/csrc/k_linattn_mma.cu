@@ -35,8 +35,6 @@
 #include <cudaTypedefs.h>
 #include <string.h>
 
-#include <type_traits>
-
 #include "linattn_mma.cuh"
 
 namespace m3 {
@@ -541,11 +539,13 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
 // Blocks: for each role, for each (segment, b, h), its column tiles. Roles come
 // after one another, not side by side: the blocks that share an SM then run the
 // same code (side by side, a third of the issue slots waited for instructions).
-template <bool SUMMARY>
+// NB: that of every role, or 0 where they differ (one launch takes them all the
+// same: a launch each took 4 % longer, for what one's last blocks leave idle).
+template <int NB, bool SUMMARY>
 __global__ void __launch_bounds__(kThreads, 2)
     k_la_mma(const __grid_constant__ LaArgs a, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) char raw[];
-  la_clear_status(a);
+  la_clear_status<SUMMARY>(a);
   const int units = a.B * a.H * a.nseg;
   int x = blockIdx.x, ri = 0, tiles = (a.role[0].P + 63) / 64;
   while (x >= units * tiles) {
@@ -557,12 +557,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   const LaRole& r = a.role[ri];
   const float ld = a.log_decay[bh % a.H], ratio = r.inter / r.intra;
   const bool mild = fabsf(ld) <= 1.f && fabsf(ratio) < 1e6f && fabsf(ratio) > 1e-6f;  // else: strong, or scale 0
-  auto go = [&](auto nb) {
-    if (mild && !SUMMARY) walk<nb.value, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
-    else walk<nb.value, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);
-  };
-  if (r.N > 64) go(std::integral_constant<int, 2>());
-  else go(std::integral_constant<int, 1>());
+  if (NB == 2 || (NB == 0 && r.N > 64)) {
+    if (mild && !SUMMARY) walk<2, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
+    else walk<2, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);
+  } else {
+    if (mild && !SUMMARY) walk<1, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
+    else walk<1, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);
+  }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -627,7 +628,12 @@ cudaError_t launch_la_mma(const LaArgs& a, LaPass pass, cudaStream_t s) {
     count_launches(1);
     return cudaGetLastError();
   };
-  return pass == kLaSummary ? go(k_la_mma<true>) : go(k_la_mma<false>);
+  int wide = 0;
+  for (int i = 0; i < a.nrole; ++i) wide += a.role[i].N > 64;
+  const bool sum = pass == kLaSummary;
+  if (wide == a.nrole) return sum ? go(k_la_mma<2, true>) : go(k_la_mma<2, false>);
+  if (wide == 0) return sum ? go(k_la_mma<1, true>) : go(k_la_mma<1, false>);
+  return sum ? go(k_la_mma<0, true>) : go(k_la_mma<0, false>);
 }
 
 }  // namespace m3

@@ -594,7 +594,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
 template <typename T, bool SUMMARY>
 __global__ void __launch_bounds__(kThreads, 1) k_la_split(const __grid_constant__ LaArgs a) {
   extern __shared__ __align__(1024) char raw[];
-  la_clear_status(a);
+  la_clear_status<SUMMARY>(a);
   const int units = a.B * a.H * a.nseg;
   int x = blockIdx.x, ri = 0, tiles = (a.role[0].P + 63) / 64;
   while (x >= units * tiles) {

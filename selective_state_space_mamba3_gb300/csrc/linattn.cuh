@@ -1,7 +1,6 @@
 // Internal declarations of the linear-attention operators (m3_qk_norm_rope,
 // m3_linear_attention_*). Validation and dispatch: m3_linattn.cu. Kernels:
-// k_qk_norm_rope.cu, k_linattn_mma.cu and k_linattn_wide.cu (prompts and adjoints,
-// bfloat16, up to and over 64 output columns),
+// k_qk_norm_rope.cu, k_linattn_mma.cu (prompts and adjoints, bfloat16),
 // k_linattn_split.cu (float32, and any width or alignment), k_linattn_state.cu
 // (states of segments, sums over shared heads), k_linattn_step.cu.
 #pragma once
@@ -74,7 +73,6 @@ struct LaArgs {
   float* entry;
   int64_t entry_role;  // floats per role in `entry`
   uint32_t* status;
-  int clear;  // this launch is the call's first: it clears the status word
 };
 
 enum LaPass { kLaMain = 0, kLaSummary = 1 };
@@ -84,7 +82,6 @@ cudaError_t launch_la_split(const LaArgs& a, LaPass pass, cudaStream_t s);
 // eight elements, 16-byte addresses): the tensor-core kernel
 bool la_mma_supported(const LaArgs& a);
 cudaError_t launch_la_mma(const LaArgs& a, LaPass pass, cudaStream_t s);
-cudaError_t launch_la_wide(const LaArgs& a, LaPass pass, cudaStream_t s);  // 64 < P
 cudaError_t launch_la_prefix(const LaArgs& a, cudaStream_t s);
 // out[row][g][w] = sum over the group's heads of part[row][h][w], in head order
 cudaError_t launch_la_group_sum(const LaArgs& a, const float* part, void* out, int groups, int rep,
@@ -133,8 +130,9 @@ __device__ __forceinline__ void la_rows(const LaArgs& a, int b, int64_t* begin, 
 
 // The call's first kernel clears the status word; a wait gives up only after
 // about two seconds.
+template <bool SUMMARY>
 __device__ __forceinline__ void la_clear_status(const LaArgs& a) {
-  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.status, 0u);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && (SUMMARY || a.nseg == 1)) atomicExch(a.status, 0u);
 }
 
 // lam^d for d >= 0 (lam = e^ld; 0 * -inf counts as 0).

@@ -124,26 +124,20 @@ int check_rows(const La& g, const int32_t* offsets) {
 }
 
 // Segments a sequence is cut into, of at least four chunks: the number with the
-// shortest pass, in chunks walked one after another. A cut call walks every
-// segment twice, the first time (states alone) in about half the time, and starts
-// two more kernels, about two chunks' time. Of numbers within 5 % of each other
-// the smallest moves the fewest states.
+// shortest pass, in chunks walked one after another. The kernels have a block for
+// every 64 output columns, and the SMs hold two (bfloat16) or one (float32) each.
+// A cut call walks every segment twice, the first time (states alone) in about
+// half the time, and starts two more kernels, about two chunks' time. Of numbers
+// within 5 % of each other the smallest moves the fewest states.
 void choose_segments(const La& g, bool backward, int* nseg, int64_t* seg_len) {
-  const bool bf16 = g.dtype == M3_DTYPE_BF16;
-  // widths of the roles' outputs, and the blocks a head takes of them
-  const int width[3] = {backward ? g.N : g.P, g.N, g.P};
-  int64_t narrow = 0, wide = 0;  // blocks of kernels that hold two an SM, and one
-  for (int i = 0; i < (backward ? 3 : 1); ++i) {
-    if (bf16 && width[i] <= 64) narrow += 1;
-    else wide += bf16 ? 1 : (width[i] + 63) / 64;
-  }
-  narrow *= (int64_t)g.B * g.H;
-  wide *= (int64_t)g.B * g.H;
+  const int tp = (g.P + 63) / 64, tn = (g.N + 63) / 64;
+  const int64_t blocks = (int64_t)g.B * g.H * (backward ? 2 * tn + tp : tp);
+  const int64_t slots = g.dtype == M3_DTYPE_BF16 ? 304 : 152;
   const int64_t chunks = (g.L + kLaChunk - 1) / kLaChunk;
   double best = 0;
   for (int64_t n = 1; n == 1 || (n <= 64 && n <= chunks / 4); ++n) {
     const int64_t per = (chunks + n - 1) / n, segs = (chunks + per - 1) / per;
-    const double turns = (double)((narrow * segs + 303) / 304 + (wide * segs + 151) / 152) * per;
+    const double turns = (double)((blocks * segs + slots - 1) / slots) * per;
     const double cost = segs > 1 ? 1.5 * turns + 2 : turns;
     if (n == 1 || cost < 0.95 * best) {
       best = cost;
@@ -194,40 +188,13 @@ LaArgs base_args(const La& g, const LaWork& w, int nrole, const float* ld, const
   return a;
 }
 
-// Roles [lo, hi) of a call, as a call of their own.
-LaArgs some_roles(const LaArgs& a, int lo, int hi, bool clear) {
-  LaArgs x = a;
-  for (int i = lo; i < hi; ++i) x.role[i - lo] = a.role[i];
-  x.nrole = hi - lo;
-  if (x.entry) x.entry += lo * x.entry_role;
-  x.clear = clear;
-  return x;
-}
-
-// One pass over every role: with tile copies, roles of more than 64 output columns
-// and of fewer have a kernel each (roles of one kind are neighbours).
-cudaError_t launch_pass(const LaArgs& a, bool tiles, LaPass pass, cudaStream_t s) {
-  const bool clear = pass == kLaSummary || a.nseg == 1;
-  if (!tiles) return launch_la_split(some_roles(a, 0, a.nrole, clear), pass, s);
-  for (int lo = 0; lo < a.nrole;) {
-    const bool wide = a.role[lo].P > 64;
-    int hi = lo + 1;
-    while (hi < a.nrole && (a.role[hi].P > 64) == wide) ++hi;
-    const LaArgs x = some_roles(a, lo, hi, clear && lo == 0);
-    const cudaError_t e = wide ? launch_la_wide(x, pass, s) : launch_la_mma(x, pass, s);
-    if (e != cudaSuccess) return e;
-    lo = hi;
-  }
-  return cudaSuccess;
-}
-
 int run_la(const LaArgs& a, cudaStream_t s) {
-  const bool tiles = la_mma_supported(a);
+  auto* const launch = la_mma_supported(a) ? launch_la_mma : launch_la_split;
   if (a.nseg > 1) {
-    M3_TRY(cuda_status(launch_pass(a, tiles, kLaSummary, s)));
+    M3_TRY(cuda_status(launch(a, kLaSummary, s)));
     M3_TRY(cuda_status(launch_la_prefix(a, s)));
   }
-  return cuda_status(launch_pass(a, tiles, kLaMain, s));
+  return cuda_status(launch(a, kLaMain, s));
 }
 
 int check_workspace(const void* ws, size_t bytes, size_t want) {
