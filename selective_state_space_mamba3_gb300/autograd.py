@@ -16,6 +16,13 @@ ABI (inner_size, state_size, num_heads, num_rope_angles, num_groups,
 mimo_rank, epsilon, dt_min, dt_max, a_floor) and the outputs are 2-D, one row
 per packed row.
 
+    q, k = qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, num_rope_angles)
+    out = linear_attention(q, k, v, log_decay, batch_size, sequence_length, ...)
+
+The last two are the layers' own operators (m3_qk_norm_rope,
+m3_linear_attention_forward and their adjoints); their activations may be
+float32 or bfloat16 and rows of a packed projection.
+
 cfg is the SsmConfig dict of the C ABI (batch_size, sequence_length, num_heads,
 num_groups, head_dim, state_size, num_rope_angles, mimo_rank, has_z, has_d,
 has_output_norm); math_mode picks the forward's arithmetic (the gradients are
@@ -136,3 +143,86 @@ def mimo_scan(cfg, c, b, x, z, adt, dt, trap, angle, c_bias, b_bias, d, mimo_x, 
     """`mamba3_mimo` with its adjoints: out [B,L,H,P]."""
     return _MimoScan.apply(dict(cfg), math_mode, c, b, x, z, adt, dt, trap, angle, c_bias,
                            b_bias, d, mimo_x, mimo_z, mimo_o, norm_weight)
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, num_rope_angles, max_positions, epsilon, cos, sin, positions, q, k, q_weight,
+                k_weight):
+        cfg = m3.qk_norm_rope_config(q, k, num_rope_angles=num_rope_angles,
+                                     max_positions=max_positions, epsilon=epsilon)
+        outs = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                for t in (q, k)]
+        m3.m3_qk_norm_rope(cfg, q, k, q_weight, k_weight, cos, sin, positions, *outs)
+        ctx.cfg, ctx.tables = cfg, (cos, sin, positions)
+        ctx.save_for_backward(q, k, q_weight, k_weight)
+        return tuple(outs)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        q, k, wq, wk = ctx.saved_tensors
+        some = q if q is not None else k
+        dy = [None if t is None else torch.zeros(t.shape, dtype=t.dtype, device=t.device)
+              if g is None else g.contiguous() for t, g in zip((q, k), grads)]
+        dx = [None if g is None else torch.empty_like(g) for g in dy]
+        dw = [None if w is None else torch.empty_like(w) for w in (wq, wk)]
+        ws = _workspace(m3.m3_qk_norm_rope_backward_workspace(ctx.cfg), some)
+        m3.m3_qk_norm_rope_backward(ctx.cfg, q, k, wq, wk, *ctx.tables, *dy, *dx, *dw, ws)
+        return (None,) * 6 + (*dx, *dw)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, cos_table, sin_table, positions, num_rope_angles,
+                 epsilon=1e-6):
+    """Norm and rotation of query and key heads (m3_qk_norm_rope) with its adjoint:
+    the normalised, rotated q and k, dense. q or k, and each weight, may be None."""
+    rows = 0 if cos_table is None else cos_table.shape[0]
+    return _QkNormRope.apply(num_rope_angles, rows, epsilon, cos_table, sin_table, positions, q, k,
+                             q_weight, k_weight)
+
+
+class _LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, batch_size, sequence_length, num_groups, scale, offsets, want_state, log_decay,
+                q, k, v, initial_state):
+        if log_decay.requires_grad:
+            raise ValueError("the decays are fixed: log_decay gets no gradient")
+        cfg = m3.linear_attention_config(q, k, v, batch_size=batch_size,
+                                         sequence_length=sequence_length, num_groups=num_groups,
+                                         scale=scale)
+        # rows of no sequence are not written
+        new = torch.empty if offsets is None else torch.zeros
+        out = new(v.shape, dtype=v.dtype, device=v.device)
+        final = None
+        if want_state:
+            final = torch.empty(batch_size, v.shape[-2], v.shape[-1], q.shape[-1], device=v.device)
+        ws = _workspace(m3.m3_linear_attention_forward_workspace(cfg), v)
+        m3.m3_linear_attention_forward(cfg, q, k, v, log_decay, offsets, initial_state, out, final, ws)
+        ctx.cfg, ctx.offsets = cfg, offsets
+        ctx.save_for_backward(log_decay, q, k, v, initial_state)
+        return out, final
+
+    @staticmethod
+    def backward(ctx, grad_out, grad_final):
+        log_decay, q, k, v, initial = ctx.saved_tensors
+        new = torch.empty if ctx.offsets is None else torch.zeros
+        if grad_out is None:
+            grad_out = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
+        grads = [new(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
+        d_init = None if initial is None else torch.empty_like(initial)
+        ws = _workspace(m3.m3_linear_attention_backward_workspace(ctx.cfg), v)
+        m3.m3_linear_attention_backward(
+            ctx.cfg, grad_out.contiguous(), q, k, v, log_decay, ctx.offsets, initial,
+            None if grad_final is None else grad_final.contiguous(), *grads, d_init, ws)
+        return (None,) * 7 + (*grads, d_init)
+
+
+def linear_attention(q, k, v, log_decay, batch_size, sequence_length, num_groups=0, scale=1.0,
+                     offsets=None, initial_state=None, return_state=False):
+    """Causal linear attention with a decay per head (m3_linear_attention_forward) with its
+    adjoints: out [..., heads, head_dim], and with return_state the final states too. The
+    decays are fixed: log_decay gets no gradient."""
+    if log_decay.requires_grad:
+        raise ValueError("the decays are fixed: log_decay gets no gradient")
+    out, final = _LinearAttention.apply(batch_size, sequence_length, num_groups, scale, offsets,
+                                        return_state, log_decay, q, k, v, initial_state)
+    return (out, final) if return_state else out

@@ -332,9 +332,9 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
     };
     const int i = 32 * quad + lane;  // this thread's row of A, P and O
     const uint32_t at_v = base + chunk_at(tid >> 2, 2 * (tid & 3)), at_o = base + chunk_at(i, 2 * grp);
-    // A decay of at most e a token splits into a factor of the row and one of the
+    // A decay of at most e^0.5 a token splits into a factor of the row and one of the
     // column over the whole chunk, lam^(i-j) = lam^(i-64) lam^(64-j), each within
-    // e^64: P takes the column's alone, S the one its readout shares, and the row's
+    // e^32 (which leaves scores times values 10^24): P takes the column's alone, S the one its readout shares, and the row's
     // is the output's. Stronger decays take a row factor for every block of 16
     // columns, and lam^d from the table on the diagonal.
     const float intra = r.intra;
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int bh = unit % (a.B * a.H), seg = unit / (a.B * a.H);
   const LaRole& r = a.role[ri];
   const float ld = a.log_decay[bh % a.H], ratio = r.inter / r.intra;
-  const bool mild = fabsf(ld) <= 1.f && fabsf(ratio) < 1e6f && fabsf(ratio) > 1e-6f;  // else: strong, or scale 0
+  const bool mild = fabsf(ld) <= 0.5f && fabsf(ratio) < 1e6f && fabsf(ratio) > 1e-6f;  // else: strong, or scale 0
   if (NB == 2 || (NB == 0 && r.N > 64)) {
     if (mild && !SUMMARY) walk<2, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
     else walk<2, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);

@@ -154,7 +154,7 @@ def test_long_sequences_are_cut_into_segments(dtype, lens):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("decay", [0.0, -1e-4, -3.0, -80.0, -200.0])
+@pytest.mark.parametrize("decay", [0.0, -1e-4, -0.5, -0.51, -3.0, -80.0, -200.0, 0.01])
 def test_decays(dtype, decay):
     Problem(1, 200, 2, 0, 64, 64, dtype, states=True, seed=6, decay=decay).check()
 
@@ -459,3 +459,79 @@ def test_weight_gradients_keep_their_bits():
                                     dw, None, ws)
         got.append(dw)
     assert torch.equal(*got)
+
+
+# --- as a layer ---------------------------------------------------------------------
+
+def test_autograd_of_a_layer():
+    """Packed projection -> norm and rotation -> ragged linear attention, differentiated
+    through the bindings, against the composed float64 formulas."""
+    import torch
+    from selective_state_space_mamba3_gb300 import autograd
+    rng = np.random.default_rng(21)
+    H, P, N, A, lens = 3, 32, 64, 16, [70, 0, 130]
+    rows = sum(lens)
+    off = np.concatenate([[0], np.cumsum(lens)])
+    proj = dev(rng.standard_normal((rows, H * (2 * N + P)))).requires_grad_()
+    wq, wk = (dev(rng.uniform(0.5, 1.5, N)).requires_grad_() for _ in range(2))
+    ang = rng.uniform(0, 6.28, (200, A))
+    cos, sin = dev(np.cos(ang)), dev(np.sin(ang))
+    posn = np.concatenate([np.arange(n) for n in lens]).astype(np.int32)
+    s0 = dev(rng.standard_normal((3, H, P, N))).requires_grad_()
+    ld = dev(-rng.uniform(0.01, 0.5, H))
+    q, k = proj[:, :H * N].view(rows, H, N), proj[:, H * N:2 * H * N].view(rows, H, N)
+    v = proj[:, 2 * H * N:].view(rows, H, P)
+    qn, kn = autograd.qk_norm_rope(q, k, wq, wk, cos, sin, torch.from_numpy(posn).cuda(), A)
+    out, fin = autograd.linear_attention(
+        qn, kn, v, ld, 3, 130, scale=0.125, offsets=torch.from_numpy(off.astype(np.int32)).cuda(),
+        initial_state=s0, return_state=True)
+    do, ds = dev(rng.standard_normal(out.shape)), dev(rng.standard_normal(fin.shape))
+    ((out * do).sum() + (fin * ds).sum()).backward()
+    hq, hk, hv = host(q.detach()), host(k.detach()), host(v.detach())
+    tabs = host(cos), host(sin)
+    yq = ref.rope(hq, host(wq.detach()), *tabs, posn, 1e-6)
+    yk = ref.rope(hk, host(wk.detach()), *tabs, posn, 1e-6)
+    want, want_fin = ref.forward(yq, yk, hv, host(ld), 0.125, 3, 130, off, host(s0.detach()))
+    assert ref.rel(host(out.detach()), want) <= ref.F32_BAR
+    assert ref.rel(host(fin.detach()), want_fin) <= ref.F32_BAR
+    dq, dk, dv, d0 = ref.backward(host(do), yq, yk, hv, host(ld), 0.125, 3, 130, off,
+                                  host(s0.detach()), host(ds))
+    gq, gwq = ref.rope_backward(hq, host(wq.detach()), *tabs, posn, 1e-6, dq)
+    gk, gwk = ref.rope_backward(hk, host(wk.detach()), *tabs, posn, 1e-6, dk)
+    want = np.concatenate([x.reshape(rows, -1) for x in (gq, gk, dv)], 1)
+    # two operators in a row: twice the bar
+    for got, w in ((proj.grad, want), (wq.grad, gwq), (wk.grad, gwk), (s0.grad, d0)):
+        assert ref.rel(host(got), w) <= 2 * ref.F32_BAR
+
+
+def test_calls_captured_into_a_graph_replay_to_the_same_bits():
+    import torch
+    p = Problem(2, 300, 4, 0, 64, 128, "bf16", states=True, seed=22)
+    out = torch.empty_like(p.d["v"])
+    fin = torch.empty_like(p.s0)
+    ws = ws_of(m3.m3_linear_attention_forward_workspace(p.cfg))
+    call = lambda: m3.m3_linear_attention_forward(  # noqa: E731
+        p.cfg, p.d["q"], p.d["k"], p.d["v"], p.ld, None, p.s0, out, fin, ws)
+    call()
+    torch.cuda.synchronize()
+    want, want_fin = out.clone(), fin.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    out.zero_(), fin.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(fin, want_fin)
+
+
+def test_the_example_runs():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "linear_attention_layer.py")
+    spec = importlib.util.spec_from_file_location("linear_attention_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    worst, losses = mod.main()
+    assert worst <= ref.BF16_BAR  # steps against the prompt call, on the same inputs
+    assert losses[-1] < losses[0]

@@ -205,3 +205,11 @@ def test_binding_refuses_other_tensors():
     packed = torch.zeros(6, 40)
     view = packed[:, 8:24].view(6, 2, 8)
     assert m3.qk_norm_rope_config(view, None, num_rope_angles=0).q_stride == 40
+
+
+def test_autograd_refuses_a_gradient_of_the_decays():
+    import torch
+    from selective_state_space_mamba3_gb300 import autograd
+    x = torch.zeros(4, 1, 8)
+    with pytest.raises(ValueError):
+        autograd.linear_attention(x, x, x, torch.zeros(1, requires_grad=True), 1, 4)
