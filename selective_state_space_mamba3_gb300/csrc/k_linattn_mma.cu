@@ -78,7 +78,7 @@ static_assert(sizeof(Small) <= 1024, "");
 constexpr uint32_t kSmem = kTiles + 1024;
 
 struct Maps {
-  CUtensorMap q[3], k[3], v[3], out[3];
+  CUtensorMap q, k, v, out;
 };
 
 // K-major 128-byte-swizzled operand: 8-row groups 1024 B apart; 16 columns on = 32 B,
@@ -119,11 +119,11 @@ __device__ __forceinline__ void tma_store_wait_read() {
 // every wait is bounded, so a thread whose wait gives up leaves the loop and the
 // others follow as theirs do.
 template <int NB, bool SUMMARY, bool MILD>
-__device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, int pt, int bh,
-                                     int seg, char* raw) {
+__device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, int bh, int seg,
+                                     char* raw) {
   constexpr int NK = 64 * NB;
   constexpr int SC = NB == 2 ? 16 : 8;  // state columns a thread
-  const LaRole& r = a.role[ri];
+  const LaRole& r = a.role;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = bh / a.H, h = bh - b * a.H;
   const int N = r.N, P = r.P, p_lo = 64 * pt;
@@ -160,9 +160,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
   const int srow = NB == 2 ? 32 * quad + lane : 16 * quad + (lane & 15);
   const int scol = NB == 2 ? 16 * grp : 16 * grp + 8 * (lane >> 4);
   float st[SC];
-  float* entry = a.entry ? a.entry + ri * a.entry_role +
-                               ((int64_t)seg * a.B * a.H + bh) * ((int64_t)N * P)
-                         : nullptr;
+  float* entry = a.entry ? a.entry + ((int64_t)seg * a.B * a.H + bh) * ((int64_t)N * P) : nullptr;
   const int64_t sbase = (int64_t)bh * N * P;
   // chunk c of a row is at the first one's address with c's bits flipped in
   const uint32_t at_state = base + chunk_at(srow, scol / 8);
@@ -220,8 +218,8 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
         tc::bar_expect_tx(&sm.bar[kBarQK], (SUMMARY ? 1 : 2) * NB * kBlock);
 #pragma unroll
         for (int x = 0; x < NB; ++x) {
-          if (!SUMMARY) tma_load(sQ + x * kBlock, &maps.q[ri], 64 * x, hq, row, &sm.bar[kBarQK]);
-          tma_load(sK + x * kBlock, &maps.k[ri], 64 * x, hk, row, &sm.bar[kBarQK]);
+          if (!SUMMARY) tma_load(sQ + x * kBlock, &maps.q, 64 * x, hq, row, &sm.bar[kBarQK]);
+          tma_load(sK + x * kBlock, &maps.k, 64 * x, hk, row, &sm.bar[kBarQK]);
         }
       }
       mark(kBarQK, ci);
@@ -229,7 +227,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
     auto load_v = [&](int ci) {
       if (lead) {
         tc::bar_expect_tx(&sm.bar[kBarV], kBlock);
-        tma_load(sV, &maps.v[ri], p_lo, hv, chunk_row(ci), &sm.bar[kBarV]);
+        tma_load(sV, &maps.v, p_lo, hv, chunk_row(ci), &sm.bar[kBarV]);
       }
       mark(kBarV, ci);
     };
@@ -238,10 +236,10 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
       if (!lead) return;
 #pragma unroll
       for (int x = 0; x < NB; ++x) {
-        if (!SUMMARY) tma_prefetch(&maps.q[ri], 64 * x, hq, row);
-        tma_prefetch(&maps.k[ri], 64 * x, hk, row);
+        if (!SUMMARY) tma_prefetch(&maps.q, 64 * x, hq, row);
+        tma_prefetch(&maps.k, 64 * x, hk, row);
       }
-      tma_prefetch(&maps.v[ri], p_lo, hv, row);
+      tma_prefetch(&maps.v, p_lo, hv, row);
     };
     auto commit = [&](int bar, int ci) {
       if (lead) tc::commit(&sm.bar[bar]);
@@ -249,7 +247,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
     };
     auto store = [&](int ci) {
       if (lead && r.out_rep == 1 && chunk_len(ci) == kC)
-        tma_store(&maps.out[ri], sX, p_lo, h, chunk_row(ci));
+        tma_store(&maps.out, sX, p_lo, h, chunk_row(ci));
     };
     load_qk(0);
     load_v(0);
@@ -334,9 +332,10 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
     const uint32_t at_v = base + chunk_at(tid >> 2, 2 * (tid & 3)), at_o = base + chunk_at(i, 2 * grp);
     // A decay of at most e^0.5 a token splits into a factor of the row and one of the
     // column over the whole chunk, lam^(i-j) = lam^(i-64) lam^(64-j), each within
-    // e^32 (which leaves scores times values 10^24): P takes the column's alone, S the one its readout shares, and the row's
-    // is the output's. Stronger decays take a row factor for every block of 16
-    // columns, and lam^d from the table on the diagonal.
+    // e^32 (which leaves scores times values 10^24): P takes the column's alone, S
+    // the one its readout shares, and the row's is the output's. Stronger decays
+    // take a row factor for every block of 16 columns, and lam^d from the table on
+    // the diagonal.
     const float intra = r.intra;
     const float rowf = MILD ? intra * expf(ld * (float)(rev ? kC / 2 - i : i - kC / 2)) : 1.f;
     float fac[2];
@@ -536,34 +535,21 @@ __device__ __forceinline__ void walk(const LaArgs& a, const Maps& maps, int ri, 
   if (warp == 0) tc::tmem_free(tm, kCols);
 }
 
-// Blocks: for each role, for each (segment, b, h), its column tiles. Roles come
-// after one another, not side by side: the blocks that share an SM then run the
-// same code (side by side, a third of the issue slots waited for instructions).
-// NB: that of every role, or 0 where they differ (one launch takes them all the
-// same: a launch each took 4 % longer, for what one's last blocks leave idle).
+// Blocks: for each (segment, b, h), its column tiles. A launch takes one role, so
+// that its settings are constants' operands instead of loads; the next role's
+// blocks may take the places that this one's leave (launch_role).
 template <int NB, bool SUMMARY>
 __global__ void __launch_bounds__(kThreads, 2)
-    k_la_mma(const __grid_constant__ LaArgs a, const __grid_constant__ Maps maps) {
+    k_la_mma(const __grid_constant__ LaCall a, const __grid_constant__ Maps maps) {
   extern __shared__ __align__(1024) char raw[];
-  la_clear_status<SUMMARY>(a);
-  const int units = a.B * a.H * a.nseg;
-  int x = blockIdx.x, ri = 0, tiles = (a.role[0].P + 63) / 64;
-  while (x >= units * tiles) {
-    x -= units * tiles;
-    tiles = (a.role[++ri].P + 63) / 64;
-  }
-  const int item = x % tiles, unit = x / tiles;
+  la_begin(a);
+  const int tiles = (a.role.P + 63) / 64, item = blockIdx.x % tiles, unit = blockIdx.x / tiles;
   const int bh = unit % (a.B * a.H), seg = unit / (a.B * a.H);
-  const LaRole& r = a.role[ri];
-  const float ld = a.log_decay[bh % a.H], ratio = r.inter / r.intra;
+  const float ld = a.log_decay[bh % a.H], ratio = a.role.inter / a.role.intra;
   const bool mild = fabsf(ld) <= 0.5f && fabsf(ratio) < 1e6f && fabsf(ratio) > 1e-6f;  // else: strong, or scale 0
-  if (NB == 2 || (NB == 0 && r.N > 64)) {
-    if (mild && !SUMMARY) walk<2, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
-    else walk<2, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);
-  } else {
-    if (mild && !SUMMARY) walk<1, SUMMARY, true>(a, maps, ri, item, bh, seg, raw);
-    else walk<1, SUMMARY, false>(a, maps, ri, item, bh, seg, raw);
-  }
+  if (mild && !SUMMARY) walk<NB, SUMMARY, true>(a, maps, item, bh, seg, raw);
+  else walk<NB, SUMMARY, false>(a, maps, item, bh, seg, raw);
+  la_end(a);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -597,7 +583,7 @@ bool tile_ok(const void* p, int width, int64_t stride) {
 }  // namespace
 
 bool la_mma_supported(const LaArgs& a) {
-  if (a.dtype != M3_DTYPE_BF16 || a.rows == 0 || !encoder()) return false;
+  if (a.call.dtype != M3_DTYPE_BF16 || a.call.rows == 0 || !encoder()) return false;
   for (int i = 0; i < a.nrole; ++i) {
     const LaRole& r = a.role[i];
     if (!tile_ok(r.q, r.N, r.qs) || !tile_ok(r.k, r.N, r.ks) || !tile_ok(r.v, r.P, r.vs) ||
@@ -607,33 +593,22 @@ bool la_mma_supported(const LaArgs& a) {
   return true;
 }
 
-cudaError_t launch_la_mma(const LaArgs& a, LaPass pass, cudaStream_t s) {
+cudaError_t launch_la_mma(const LaCall& a, LaPass pass, cudaStream_t s) {
   Maps maps;
   memset(&maps, 0, sizeof(maps));
-  int items = 0;
-  for (int i = 0; i < a.nrole; ++i) {
-    const LaRole& r = a.role[i];
-    items += (r.P + 63) / 64;
-    if (!make_map(&maps.q[i], r.q, r.N, a.H / r.q_rep, a.rows, r.qs) ||
-        !make_map(&maps.k[i], r.k, r.N, a.H / r.k_rep, a.rows, r.ks) ||
-        !make_map(&maps.v[i], r.v, r.P, a.H / r.v_rep, a.rows, r.vs) ||
-        (r.out_rep == 1 && !make_map(&maps.out[i], r.out, r.P, a.H, a.rows, r.os)))
-      return cudaErrorInvalidValue;
-  }
-  const unsigned grid = (unsigned)((int64_t)a.B * a.H * a.nseg * items);
-  auto go = [&](auto kernel) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, kSmem, s>>>(a, maps);
-    count_launches(1);
-    return cudaGetLastError();
-  };
-  int wide = 0;
-  for (int i = 0; i < a.nrole; ++i) wide += a.role[i].N > 64;
+  const LaRole& r = a.role;
+  if (!make_map(&maps.q, r.q, r.N, a.H / r.q_rep, a.rows, r.qs) ||
+      !make_map(&maps.k, r.k, r.N, a.H / r.k_rep, a.rows, r.ks) ||
+      !make_map(&maps.v, r.v, r.P, a.H / r.v_rep, a.rows, r.vs) ||
+      (r.out_rep == 1 && !make_map(&maps.out, r.out, r.P, a.H, a.rows, r.os)))
+    return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)((int64_t)a.B * a.H * a.nseg * ((r.P + 63) / 64));
   const bool sum = pass == kLaSummary;
-  if (wide == a.nrole) return sum ? go(k_la_mma<2, true>) : go(k_la_mma<2, false>);
-  if (wide == 0) return sum ? go(k_la_mma<1, true>) : go(k_la_mma<1, false>);
-  return sum ? go(k_la_mma<0, true>) : go(k_la_mma<0, false>);
+  if (r.N > 64)
+    return sum ? launch_role(k_la_mma<2, true>, grid, kThreads, kSmem, a.beside, s, a, maps)
+               : launch_role(k_la_mma<2, false>, grid, kThreads, kSmem, a.beside, s, a, maps);
+  return sum ? launch_role(k_la_mma<1, true>, grid, kThreads, kSmem, a.beside, s, a, maps)
+             : launch_role(k_la_mma<1, false>, grid, kThreads, kSmem, a.beside, s, a, maps);
 }
 
 }  // namespace m3

@@ -121,13 +121,13 @@ __device__ __forceinline__ bool vec_rows(const void* p, int width, int64_t strid
 // issues the products, and they meet at mbarriers with bounded waits). NB:
 // 64-column blocks of N.
 template <typename T, int NB, bool SUMMARY>
-__device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, int seg, char* raw) {
+__device__ __forceinline__ void walk(const LaCall& a, int pt, int bh, int seg, char* raw) {
   constexpr int IP = sizeof(T) == 4 ? 3 : 1;  // parts of an input
   constexpr int NK = 64 * NB;
   constexpr int SC = NB == 2 ? 16 : 8;                             // state columns a thread
   constexpr int KQ = (kC * NK / 4 + 32 * kWarps - 1) / (32 * kWarps);  // quads of K a thread
   constexpr int VQ = (kC * 16 + 32 * kWarps - 1) / (32 * kWarps);      // quads of V a thread
-  const LaRole& r = a.role[ri];
+  const LaRole& r = a.role;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int quad = warp & 3, grp = (warp >> 2) & 3;
   const int b = bh / a.H, h = bh - b * a.H;
@@ -366,9 +366,7 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
     const int srow = NB == 2 ? 32 * quad + lane : 16 * quad + (lane & 15);
     const int scol = NB == 2 ? 16 * grp : 16 * grp + 8 * (lane >> 4);
     float st[SC];
-    float* entry = a.entry ? a.entry + ri * a.entry_role +
-                                 ((int64_t)seg * a.B * a.H + bh) * ((int64_t)N * P)
-                           : nullptr;
+    float* entry = a.entry ? a.entry + ((int64_t)seg * a.B * a.H + bh) * ((int64_t)N * P) : nullptr;
     const int64_t sbase = (int64_t)bh * N * P;
 #pragma unroll
     for (int j = 0; j < SC; ++j) {
@@ -591,39 +589,30 @@ __device__ __forceinline__ void walk(const LaArgs& a, int ri, int pt, int bh, in
   if (warp == 0) tc::tmem_free(tm, kCols);
 }
 
-template <typename T, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads, 1) k_la_split(const __grid_constant__ LaArgs a) {
+template <typename T, int NB, bool SUMMARY>
+__global__ void __launch_bounds__(kThreads, 1) k_la_split(const __grid_constant__ LaCall a) {
   extern __shared__ __align__(1024) char raw[];
-  la_clear_status<SUMMARY>(a);
-  const int units = a.B * a.H * a.nseg;
-  int x = blockIdx.x, ri = 0, tiles = (a.role[0].P + 63) / 64;
-  while (x >= units * tiles) {
-    x -= units * tiles;
-    tiles = (a.role[++ri].P + 63) / 64;
-  }
-  const int item = x % tiles, unit = x / tiles;
-  const int bh = unit % (a.B * a.H), seg = unit / (a.B * a.H);
-  const LaRole& r = a.role[ri];
-  if (r.N > 64) walk<T, 2, SUMMARY>(a, ri, item, bh, seg, raw);
-  else walk<T, 1, SUMMARY>(a, ri, item, bh, seg, raw);
+  la_begin(a);
+  const int tiles = (a.role.P + 63) / 64, item = blockIdx.x % tiles, unit = blockIdx.x / tiles;
+  walk<T, NB, SUMMARY>(a, item, unit % (a.B * a.H), unit / (a.B * a.H), raw);
+  la_end(a);
+}
+
+template <typename T>
+cudaError_t go(const LaCall& a, bool sum, cudaStream_t s) {
+  const unsigned grid = (unsigned)((int64_t)a.B * a.H * a.nseg * ((a.role.P + 63) / 64));
+  if (a.role.N > 64)
+    return sum ? launch_role(k_la_split<T, 2, true>, grid, kThreads, kSmem, a.beside, s, a)
+               : launch_role(k_la_split<T, 2, false>, grid, kThreads, kSmem, a.beside, s, a);
+  return sum ? launch_role(k_la_split<T, 1, true>, grid, kThreads, kSmem, a.beside, s, a)
+             : launch_role(k_la_split<T, 1, false>, grid, kThreads, kSmem, a.beside, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_la_split(const LaArgs& a, LaPass pass, cudaStream_t s) {
-  int items = 0;
-  for (int i = 0; i < a.nrole; ++i) items += (a.role[i].P + 63) / 64;
-  const unsigned grid = (unsigned)((int64_t)a.B * a.H * a.nseg * items);
-  auto go = [&](auto kernel) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
-    if (e != cudaSuccess) return e;
-    kernel<<<grid, kThreads, kSmem, s>>>(a);
-    count_launches(1);
-    return cudaGetLastError();
-  };
-  if (a.dtype == M3_DTYPE_FP32)
-    return pass == kLaSummary ? go(k_la_split<float, true>) : go(k_la_split<float, false>);
-  return pass == kLaSummary ? go(k_la_split<__nv_bfloat16, true>) : go(k_la_split<__nv_bfloat16, false>);
+cudaError_t launch_la_split(const LaCall& a, LaPass pass, cudaStream_t s) {
+  return a.dtype == M3_DTYPE_FP32 ? go<float>(a, pass == kLaSummary, s)
+                                  : go<__nv_bfloat16>(a, pass == kLaSummary, s);
 }
 
 }  // namespace m3

@@ -7,10 +7,11 @@ namespace {
 
 // Entry states of the segments from their own sums, in walking order: one
 // thread per state element, the sums of eight segments in flight at a time.
-__global__ void __launch_bounds__(256) k_la_prefix(const __grid_constant__ LaArgs a) {
+__global__ void __launch_bounds__(256) k_la_prefix(const __grid_constant__ LaArgs args) {
   constexpr int kAhead = 8;
+  const LaCall& a = args.call;
   const int bh = blockIdx.x % (a.B * a.H), ri = blockIdx.x / (a.B * a.H);
-  const LaRole& r = a.role[ri];
+  const LaRole& r = args.role[ri];
   const int np = r.N * r.P, i = blockIdx.y * 256 + threadIdx.x;
   if (i >= np) return;
   int64_t row0, len;
@@ -20,7 +21,7 @@ __global__ void __launch_bounds__(256) k_la_prefix(const __grid_constant__ LaArg
   const int p = i / r.N, n = i - p * r.N;
   float st = r.init ? r.init[(int64_t)bh * np + (int64_t)p * r.sp + (int64_t)n * r.sn] : 0.f;
   const int64_t step = (int64_t)a.B * a.H * np;
-  float* e = a.entry + ri * a.entry_role + (int64_t)bh * np + i;
+  float* e = a.entry + ri * args.entry_role + (int64_t)bh * np + i;
   // every segment but the sequence's last rows' one has seg_len tokens
   const float whole = la_power(ld, a.seg_len), tail = la_power(ld, len - last * a.seg_len);
   for (int x0 = 0; x0 <= last; x0 += kAhead) {
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(256) k_la_prefix(const __grid_constant__ LaArg
 // One row a block. With offsets, rows of no sequence keep what they hold.
 template <typename T>
 __global__ void __launch_bounds__(128)
-    k_la_group_sum(const __grid_constant__ LaArgs a, const float* part, T* out, int groups, int rep, int width) {
+    k_la_group_sum(const __grid_constant__ LaCall a, const float* part, T* out, int groups, int rep, int width) {
   const int64_t row = blockIdx.x;
   if (a.offsets) {
     int lo = 0, hi = a.B;  // the last sequence that begins at or before the row
@@ -76,12 +77,12 @@ cudaError_t launch_la_prefix(const LaArgs& a, cudaStream_t s) {
     const int x = a.role[i].N * a.role[i].P;
     np = x > np ? x : np;
   }
-  k_la_prefix<<<dim3((unsigned)(a.B * a.H * a.nrole), (unsigned)((np + 255) / 256)), 256, 0, s>>>(a);
+  k_la_prefix<<<dim3((unsigned)(a.call.B * a.call.H * a.nrole), (unsigned)((np + 255) / 256)), 256, 0, s>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
 
-cudaError_t launch_la_group_sum(const LaArgs& a, const float* part, void* out, int groups, int rep,
+cudaError_t launch_la_group_sum(const LaCall& a, const float* part, void* out, int groups, int rep,
                                 int width, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;
   if (a.dtype == M3_DTYPE_FP32)

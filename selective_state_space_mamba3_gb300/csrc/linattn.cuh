@@ -58,33 +58,40 @@ struct LaRole {
 
 constexpr int kLaChunk = 128;  // segments are whole numbers of this many tokens
 
-struct LaArgs {
-  LaRole role[3];
-  int nrole;
+// One launch of the chunk kernels: a role and what every role of the call shares.
+struct LaCall {
+  LaRole role;
   int B, H, dtype;
   int64_t L, rows;
   const float* log_decay;
   const int32_t* offsets;
   // long sequences are cut into nseg segments of seg_len tokens: `entry` has,
-  // for each (role, segment, b, h), first the segment's own state sum
-  // (summary pass), then its entry state (prefix pass); states as [P][N]
+  // for each (segment, b, h), first the segment's own state sum (summary pass),
+  // then its entry state (prefix pass); states as [P][N]
   int nseg;
   int64_t seg_len;
   float* entry;
-  int64_t entry_role;  // floats per role in `entry`
   uint32_t* status;
+  int clear;   // the call's first launch clears the status word
+  int beside;  // the launch before it is the same pass of another role: run beside it
+};
+struct LaArgs {
+  LaRole role[3];
+  int nrole;
+  LaCall call;         // (its role and entry: of the role at hand)
+  int64_t entry_role;  // floats per role in `entry`
 };
 
 enum LaPass { kLaMain = 0, kLaSummary = 1 };
 // float32 activations, and bfloat16 ones that the other kernel does not take
-cudaError_t launch_la_split(const LaArgs& a, LaPass pass, cudaStream_t s);
+cudaError_t launch_la_split(const LaCall& a, LaPass pass, cudaStream_t s);
 // bfloat16 operands that tile copies take (widths and strides multiples of
 // eight elements, 16-byte addresses): the tensor-core kernel
 bool la_mma_supported(const LaArgs& a);
-cudaError_t launch_la_mma(const LaArgs& a, LaPass pass, cudaStream_t s);
+cudaError_t launch_la_mma(const LaCall& a, LaPass pass, cudaStream_t s);
 cudaError_t launch_la_prefix(const LaArgs& a, cudaStream_t s);
 // out[row][g][w] = sum over the group's heads of part[row][h][w], in head order
-cudaError_t launch_la_group_sum(const LaArgs& a, const float* part, void* out, int groups, int rep,
+cudaError_t launch_la_group_sum(const LaCall& a, const float* part, void* out, int groups, int rep,
                                 int width, cudaStream_t s);
 
 struct LaStepArgs {
@@ -116,7 +123,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 
 // Rows [begin, end) of sequence b; offsets outside [0, rows] count as the
 // nearest row inside, and a sequence is at most L rows long.
-__device__ __forceinline__ void la_rows(const LaArgs& a, int b, int64_t* begin, int64_t* len) {
+__device__ __forceinline__ void la_rows(const LaCall& a, int b, int64_t* begin, int64_t* len) {
   if (!a.offsets) {
     *begin = (int64_t)b * a.L;
     *len = a.L;
@@ -128,16 +135,43 @@ __device__ __forceinline__ void la_rows(const LaArgs& a, int b, int64_t* begin, 
   *len = min(hi - lo, a.L);
 }
 
-// The call's first kernel clears the status word; a wait gives up only after
-// about two seconds.
-template <bool SUMMARY>
-__device__ __forceinline__ void la_clear_status(const LaArgs& a) {
-  if (blockIdx.x == 0 && threadIdx.x == 0 && (SUMMARY || a.nseg == 1)) atomicExch(a.status, 0u);
+// Start and end of a block of a chunk kernel. The call's first kernel clears the
+// status word (a wait gives up only after about two seconds); every block lets the
+// next launch begin, and one that began beside its predecessor ends after it, so
+// that the end of the last role's kernel is the end of all.
+__device__ __forceinline__ void la_begin(const LaCall& a) {
+  if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) atomicExch(a.status, 0u);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void la_end(const LaCall& a) {
+  if (a.beside) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // lam^d for d >= 0 (lam = e^ld; 0 * -inf counts as 0).
 __device__ __forceinline__ float la_power(float ld, int64_t d) {
   return d == 0 ? 1.0f : expf(ld * (float)d);
+}
+
+// Launches a chunk kernel, beside the launch before it where that is another
+// role's pass (programmatic stream serialization).
+template <typename... Ps, typename... As>
+cudaError_t launch_role(void (*kernel)(Ps...), unsigned grid, int threads, size_t smem, bool beside,
+                        cudaStream_t s, const As&... args) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
 }
 
 }  // namespace m3

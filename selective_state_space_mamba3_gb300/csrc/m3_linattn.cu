@@ -179,22 +179,37 @@ LaArgs base_args(const La& g, const LaWork& w, int nrole, const float* ld, const
                  void* ws) {
   LaArgs a{};
   a.nrole = nrole;
-  a.B = g.B; a.H = g.H; a.dtype = g.dtype; a.L = g.L; a.rows = g.rows;
-  a.log_decay = ld; a.offsets = offsets;
-  a.nseg = w.nseg; a.seg_len = w.seg_len;
-  a.entry = w.nseg > 1 ? (float*)((char*)ws + w.entry) : nullptr;
+  LaCall& c = a.call;
+  c.B = g.B; c.H = g.H; c.dtype = g.dtype; c.L = g.L; c.rows = g.rows;
+  c.log_decay = ld; c.offsets = offsets;
+  c.nseg = w.nseg; c.seg_len = w.seg_len;
+  c.entry = w.nseg > 1 ? (float*)((char*)ws + w.entry) : nullptr;
+  c.status = (uint32_t*)ws;
   a.entry_role = (int64_t)w.nseg * g.B * g.H * g.N * g.P;
-  a.status = (uint32_t*)ws;
   return a;
 }
 
-int run_la(const LaArgs& a, cudaStream_t s) {
+// One pass of every role.
+cudaError_t launch_pass(const LaArgs& a, LaPass pass, cudaStream_t s) {
   auto* const launch = la_mma_supported(a) ? launch_la_mma : launch_la_split;
-  if (a.nseg > 1) {
-    M3_TRY(cuda_status(launch(a, kLaSummary, s)));
+  for (int i = 0; i < a.nrole; ++i) {
+    LaCall c = a.call;
+    c.role = a.role[i];
+    if (c.entry) c.entry += i * a.entry_role;
+    c.clear = i == 0 && (pass == kLaSummary || c.nseg == 1);
+    c.beside = i > 0;
+    const cudaError_t e = launch(c, pass, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+int run_la(const LaArgs& a, cudaStream_t s) {
+  if (a.call.nseg > 1) {
+    M3_TRY(cuda_status(launch_pass(a, kLaSummary, s)));
     M3_TRY(cuda_status(launch_la_prefix(a, s)));
   }
-  return cuda_status(launch(a, kLaMain, s));
+  return cuda_status(launch_pass(a, kLaMain, s));
 }
 
 int check_workspace(const void* ws, size_t bytes, size_t want) {
@@ -392,8 +407,8 @@ int m3_linear_attention_backward(const m3_linear_attention_config* cfg, const vo
   cudaStream_t s = (cudaStream_t)stream;
   M3_TRY(run_la(a, s));
   if (!shared) return M3_OK;
-  M3_TRY(cuda_status(launch_la_group_sum(a, part_q, grad_q, g.G, g.rep, g.N, s)));
-  return cuda_status(launch_la_group_sum(a, part_k, grad_k, g.G, g.rep, g.N, s));
+  M3_TRY(cuda_status(launch_la_group_sum(a.call, part_q, grad_q, g.G, g.rep, g.N, s)));
+  return cuda_status(launch_la_group_sum(a.call, part_k, grad_k, g.G, g.rep, g.N, s));
 }
 
 }  // extern "C"
