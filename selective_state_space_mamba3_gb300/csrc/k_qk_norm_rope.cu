@@ -71,6 +71,12 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
   *(uint4*)p = *(const uint4*)h;
 }
 
+__device__ __forceinline__ float2 pair(const float* v, int i) { return make_float2(v[i], v[i + 1]); }
+__device__ __forceinline__ void set(float* v, int i, float2 p) {
+  v[i] = p.x;
+  v[i + 1] = p.y;
+}
+
 // Sum over the aligned group of `g` lanes (a power of two) the lane is in.
 __device__ __forceinline__ float group_sum(float v, int g) {
   for (int o = g / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -185,19 +191,21 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 4)
         const bool in = h < h1 && hb + u < per;
         float v[8], m[8];
         values(rx[u], v);
-        float ss = 0.f;
+        float2 s2 = __fmul2_rn(pair(v, 0), pair(v, 0));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-        ss = group_sum(ss, lanes);
+        for (int i = 2; i < 8; i += 2) s2 = __ffma2_rn(pair(v, i), pair(v, i), s2);
+        const float ss = group_sum(s2.x + s2.y, lanes);
         const float inv = rsqrtf(fmaf(ss, inv_d, a.eps));
         if (!BWD) {
+          const float2 i2 = make_float2(inv, inv);
           if (A > 0) {
             values(from_lane(rx[u], mate), m);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = inv * fmaf(m[i], sn[i], v[i] * c[i]);
+            for (int i = 0; i < 8; i += 2)
+              set(v, i, __fmul2_rn(i2, __ffma2_rn(pair(m, i), pair(sn, i), __fmul2_rn(pair(v, i), pair(c, i)))));
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = inv * (v[i] * c[i]);
+            for (int i = 0; i < 8; i += 2) set(v, i, __fmul2_rn(i2, __fmul2_rn(pair(v, i), pair(c, i))));
           }
         } else {
           float g[8];
@@ -205,19 +213,24 @@ __global__ void __launch_bounds__(kThreads, BWD ? 2 : 4)
           if (A > 0) {
             values(from_lane(rg[BWD ? u : 0], mate), m);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = fmaf(m[i], sn[i], g[i] * c[i]);
+            for (int i = 0; i < 8; i += 2)
+              set(g, i, __ffma2_rn(pair(m, i), pair(sn, i), __fmul2_rn(pair(g, i), pair(c, i))));
           }
-          float dot = 0.f;
+          const float2 i2 = make_float2(inv, inv);
+          float2 d2 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            v[i] *= inv;
-            gw[i] = fmaf(g[i], v[i], gw[i]);
-            g[i] *= w[i];
-            dot = fmaf(g[i], v[i], dot);
+          for (int i = 0; i < 8; i += 2) {
+            const float2 xh = __fmul2_rn(pair(v, i), i2), gi = pair(g, i);
+            set(v, i, xh);
+            set(gw, i, __ffma2_rn(gi, xh, pair(gw, i)));
+            const float2 wg = __fmul2_rn(gi, pair(w, i));
+            set(g, i, wg);
+            d2 = __ffma2_rn(wg, xh, d2);
           }
-          dot = group_sum(dot, lanes) * inv_d;
+          const float dot = -group_sum(d2.x + d2.y, lanes) * inv_d;
+          const float2 dd = make_float2(dot, dot);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = inv * fmaf(-v[i], dot, g[i]);
+          for (int i = 0; i < 8; i += 2) set(v, i, __fmul2_rn(i2, __ffma2_rn(pair(v, i), dd, pair(g, i))));
         }
         if (in) store8(y + h * D, v);
       }
