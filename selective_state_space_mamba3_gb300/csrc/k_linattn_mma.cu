@@ -168,7 +168,7 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
   auto put_state = [&](float f) {
     float x[SC];
 #pragma unroll
-    for (int j = 0; j < SC; ++j) x[j] = MILD ? f * st[j] : st[j];
+    for (int j = 0; j < SC; j += 2) set(x, j, MILD ? __fmul2_rn(make_float2(f, f), pair(st, j)) : pair(st, j));
 #pragma unroll
     for (int c = 0; c < SC / 8; ++c)
       sts<kS>(at_state ^ (c << 4),
@@ -475,7 +475,8 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
         }
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < SC; ++j) st[j] = fmaf(dec, st[j], kv[j]);
+        for (int j = 0; j < SC; j += 2)
+          set(st, j, __ffma2_rn(make_float2(dec, dec), pair(st, j), pair(kv, j)));
         if (!SUMMARY) put_state(ratio * power(rev ? kC / 2 : kC / 2 + 1));
       }
       tc::fence_before();
@@ -492,7 +493,7 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
         arrive(kBarE);
         if (MILD) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= rowf;
+          for (int e = 0; e < 16; e += 2) set(o, e, __fmul2_rn(make_float2(rowf, rowf), pair(o, e)));
         }
         const int64_t at_out = (chunk_row(ci) + i) * r.os + (int64_t)h * P + p_lo + c0;
         if (r.out_rep > 1) {  // float32 partials of a shared head

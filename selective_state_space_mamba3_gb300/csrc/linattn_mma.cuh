@@ -82,6 +82,11 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
 }
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ float2 pair(const float* v, int i) { return make_float2(v[i], v[i + 1]); }
+__device__ __forceinline__ void set(float* v, int i, float2 p) {
+  v[i] = p.x;
+  v[i + 1] = p.y;
+}
 // Byte offset of the 16-byte chunk `c` of row r in a swizzled block.
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 // Bounded wait. One try nearly always sees the phase end; what follows where it
