@@ -137,6 +137,8 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
   if (SUMMARY && seg == (rev ? 0 : last_seg)) return;  // the prefix pass never reads it
   const bool first = seg == (rev ? last_seg : 0), last = seg == (rev ? 0 : last_seg);
   const int nchunk = (ntok + kC - 1) / kC;
+  // this block's state is returned, or goes into one that is: three parts of V^
+  const bool fin = r.fin && (SUMMARY || last);
 
   const uint32_t base = tc::smem_u32(raw);
   const uint32_t sQ = base + kQ, sK = base + kK, sV = base + kV, sX = base + kX, sS = base + kS;
@@ -251,7 +253,7 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
     };
     load_qk(0);
     load_v(0);
-    const int ksq = (N + 15) / 16, parts = r.fin ? 3 : 2;
+    const int ksq = (N + 15) / 16, parts = fin ? 3 : 2;
     const uint32_t dQ = kmajor(sQ), dK = kmajor(sK), dKt = mnmajor(sK), dV = mnmajor(sV), dS = mnmajor(sS);
     for (int ci = 0; ci < nchunk; ++ci) {
       const uint32_t ph = ci & 1;
@@ -387,7 +389,7 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) sts<kQ>(at_v ^ (c << 4), low[c]);
-        if (r.fin) {  // the state is returned: a third part
+        if (fin) {  // a third part
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const uint4 v = lds<kV>(at_v ^ (c << 4)), l = low[c];
