@@ -539,7 +539,8 @@ int m3_linear_attention_step(const m3_linear_attention_config* cfg, const void* 
  *   grad_initial_state = lam^len grad_final_state + scale sum_t lam^(t+1) grad_out_t q_t^T
  * (grad_q, grad_k summed over the heads of a group, in head order). grad_out
  * has out's stride; grad_q, grad_k, grad_v are dense. initial_state and
- * grad_final_state may be NULL (zero), grad_initial_state NULL (not wanted).
+ * grad_final_state may be NULL (zero), grad_initial_state NULL (not wanted);
+ * no output may overlap an input.
  * The decays are taken as fixed: they get no gradient.
  */
 int m3_linear_attention_backward_workspace(const m3_linear_attention_config* cfg, size_t* bytes);

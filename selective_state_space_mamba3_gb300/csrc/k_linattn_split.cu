@@ -250,11 +250,12 @@ __device__ __forceinline__ void walk(const LaCall& a, int pt, int bh, int seg, c
     const T* gv = (const T*)r.v + (int64_t)(h / r.v_rep) * P;
     const bool qvec = vec_rows<T>(gq, N, r.qs), kvec = vec_rows<T>(gk, N, r.ks), vvec = vec_rows<T>(gv, P, r.vs);
     float4 rk[KQ], rv[VQ], rq[4];  // this thread's values of the next chunk
-    auto load_k = [&](int ci) {
+    auto load_k = [&](int ci, int from, int to) {  // quads [from, to)
       const T* g = gk + (int64_t)chunk_row(ci) * r.ks;
       const int n = chunk_len(ci);
 #pragma unroll
       for (int x = 0; x < KQ; ++x) {
+        if (x < from || x >= to) continue;
         const int t = tid / (NK / 4) + x * (32 * kWarps / (NK / 4)), c = tid % (NK / 4) * 4;
         rk[x] = t < n ? load4<T>(g + t * r.ks, c, N, kvec) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
@@ -398,7 +399,7 @@ __device__ __forceinline__ void walk(const LaCall& a, int pt, int bh, int seg, c
       fac[x] = d < 0 ? 0.f : r.intra * sm.pw[d];
     }
     if (nchunk > 0) {
-      load_k(0);
+      load_k(0, 0, KQ);
       load_v(0);
       put_k();
       if (!SUMMARY) {
@@ -477,6 +478,8 @@ __device__ __forceinline__ void walk(const LaCall& a, int pt, int bh, int seg, c
         tc::fence_before();
         arrive(kBarP);
       }
+      constexpr int kEarly = KQ / 2;  // keys loaded while K^T V^ runs: as many as registers are left
+      if (more) load_k(ci + 1, 0, kEarly);
       if (!wait(kBarB, ph)) break;
       tc::fence_after();
       {
@@ -491,7 +494,7 @@ __device__ __forceinline__ void walk(const LaCall& a, int pt, int bh, int seg, c
       }
       tc::fence_before();
       if (more) {
-        load_k(ci + 1);
+        load_k(ci + 1, kEarly, KQ);
         put_k();
       }
       if (SUMMARY) {
