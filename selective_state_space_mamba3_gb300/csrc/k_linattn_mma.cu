@@ -21,12 +21,16 @@
 // operands, so nothing is transposed by the threads. The low parts of V^ take
 // the Q tile once A and Oi are done, and the output is staged in the high part's
 // tile for a TMA store. That is 112 KB at N = 128: two blocks an SM, whose
-// phases (copies, products, masks) overlap each other. Eight warps compute and a
-// ninth issues copies and products: with the products issued by a compute warp
-// (some 40 of them, 30 to 70 cycles each) the other seven waited for it.
+// phases (copies, products, masks) overlap each other. Sixteen warps compute and a
+// seventeenth issues copies and products: issued by a compute warp (some 40 of them,
+// 50 to 65 cycles each) the others waited for it.
 //
-// The pass is bound by HBM: 2 (2 N + 2 P) bytes a token and head against 1,540
-// tensor cycles a chunk at N = 128, P = 64.
+// The floor is HBM's: 2 (2 N + 2 P) bytes a token and head, 4,200 cycles a chunk and
+// SM at N = 128, P = 64; the products take about 2,600 (a step of 128 x 64 x 16 as
+// long as one of 128 x 128 x 16), the threads' instructions about 2,000. Measured on
+// prompts of 8 x 2048 tokens, 32 heads, P 64, N 128: 75 us, 5.3 TB/s, 79 % of a copy's
+// rate; adjoints of the same 262 us. With few blocks a chunk's own chain binds, some
+// 7,000 cycles alone on an SM.
 //
 // A chunk of n < 128 tokens (a sequence's end) zeroes its K and V rows up to a
 // multiple of 16, which is as far as its products reach: rows of the next

@@ -16,8 +16,12 @@
 // fetched into L2; K's are cut and stored as soon as K^T V^ has read the tile, those
 // of Q and V as soon as P V has.
 //
-// Bound by the tensor cores: six passes cost 6,900 cycles a chunk at N = 128,
-// P = 64, against 7,300 for its bytes at the HBM rate.
+// At N = 128, P = 64 a chunk's 138 products take some 9,000 cycles of its 19,000; the
+// rest is the cutting, for which the tiles that the products read have to be free,
+// and loads that go through what 217 KB of shared memory leave of the L1. Measured on
+// 2 x 16,384 tokens, 32 heads, 4 groups: 0.81 ms, where float32 arithmetic on the CUDA
+// cores took 4.6 ms and the bytes would take 0.10. Nothing may spill: with no L1 to
+// hold them, spilled registers cost as much as the loads they hide.
 #include "linattn_mma.cuh"
 
 namespace m3 {
