@@ -123,20 +123,22 @@ int check_rows(const La& g, const int32_t* offsets) {
   return g.rows == (int64_t)g.B * g.L ? M3_OK : M3_ERR_INVALID_ARGUMENT;
 }
 
-// Segments a sequence is cut into, of at least four chunks: the number with the
-// shortest pass, in chunks walked one after another. The kernels have a block for
-// every 64 output columns, and the SMs hold two (bfloat16) or one (float32) each.
-// A cut call walks every segment twice, the first time (states alone) in about
-// half the time, and starts two more kernels, about two chunks' time. Of numbers
-// within 5 % of each other the smallest moves the fewest states.
+// Segments a sequence is cut into: the number with the shortest pass, in chunks
+// walked one after another. The kernels have a block for every 64 output columns,
+// and the SMs hold two (bfloat16) or one (float32) each. A cut call walks every
+// segment twice, the first time (states alone) in about half the time, and starts
+// two more kernels, about two chunks' time. Of numbers within 5 % of each other the
+// smallest moves the fewest states; segments of fewer than four chunks, whose states
+// are as large as their rows, are for calls that leave SMs without a block.
 void choose_segments(const La& g, bool backward, int* nseg, int64_t* seg_len) {
   const int tp = (g.P + 63) / 64, tn = (g.N + 63) / 64;
   const int64_t blocks = (int64_t)g.B * g.H * (backward ? 2 * tn + tp : tp);
   const int64_t slots = g.dtype == M3_DTYPE_BF16 ? 304 : 152;
   const int64_t chunks = (g.L + kLaChunk - 1) / kLaChunk;
   double best = 0;
-  for (int64_t n = 1; n == 1 || (n <= 64 && n <= chunks / 4); ++n) {
+  for (int64_t n = 1; n <= 64 && n <= chunks; ++n) {
     const int64_t per = (chunks + n - 1) / n, segs = (chunks + per - 1) / per;
+    if (segs > 1 && per < 4 && blocks * segs > slots) continue;
     const double turns = (double)((blocks * segs + slots - 1) / slots) * per;
     const double cost = segs > 1 ? 1.5 * turns + 2 : turns;
     if (n == 1 || cost < 0.95 * best) {
