@@ -331,15 +331,15 @@ __global__ void __launch_bounds__(kThreads) k_rope_any(const __grid_constant__ R
   }
 }
 
-// Weight gradients from the blocks' sums: 32 columns a block, each of its
-// eight warps a run of the side's blocks in order, then the warps in order.
-__global__ void __launch_bounds__(256) k_rope_weights(const __grid_constant__ RopeArgs a, Split split) {
-  __shared__ float part[8][32];
+// Weight gradients from the blocks' sums: 32 columns a block, each of its 32
+// warps a run of the side's blocks in order, then the warps in order.
+__global__ void __launch_bounds__(1024) k_rope_weights(const __grid_constant__ RopeArgs a, Split split) {
+  __shared__ float part[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int side = blockIdx.y, d = blockIdx.x * 32 + lane;
   if (!a.gw[side]) return;
   const int first = side ? split.q_blocks : 0, end = side ? split.blocks : split.q_blocks;
-  const int per = (end - first + 7) / 8;
+  const int per = (end - first + 31) / 32;
   float s = 0.f;
   if (d < a.D)
     for (int x = first + warp * per; x < min(end, first + (warp + 1) * per); ++x)
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(256) k_rope_weights(const __grid_constant__ Ro
   __syncthreads();
   if (warp == 0 && d < a.D) {
     s = 0.f;
-    for (int x = 0; x < 8; ++x) s += part[x][lane];
+    for (int x = 0; x < 32; ++x) s += part[x][lane];
     a.gw[side][d] = s;
   }
 }
@@ -401,7 +401,7 @@ cudaError_t go(const RopeArgs& a, cudaStream_t s) {
   count_launches(1);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !BWD || !a.partial) return e;
-  k_rope_weights<<<dim3((unsigned)((a.D + 31) / 32), 2), 256, 0, s>>>(a, split);
+  k_rope_weights<<<dim3((unsigned)((a.D + 31) / 32), 2), 1024, 0, s>>>(a, split);
   count_launches(1);
   return cudaGetLastError();
 }

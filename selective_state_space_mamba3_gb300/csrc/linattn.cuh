@@ -1,8 +1,9 @@
 // Internal declarations of the linear-attention operators (m3_qk_norm_rope,
 // m3_linear_attention_*). Validation and dispatch: m3_linattn.cu. Kernels:
 // k_qk_norm_rope.cu, k_linattn_mma.cu (prompts and adjoints, bfloat16),
-// k_linattn_split.cu (float32, and any width or alignment), k_linattn_state.cu
-// (states of segments, sums over shared heads), k_linattn_step.cu.
+// k_linattn_split.cu (float32, and any width or alignment), k_linattn_short.cu (the
+// same for a few tokens), k_linattn_state.cu (states of segments, sums over shared
+// heads), k_linattn_step.cu.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -83,6 +84,9 @@ struct LaArgs {
 };
 
 enum LaPass { kLaMain = 0, kLaSummary = 1 };
+// sequences of at most kLaShort tokens that the bfloat16 kernel does not take
+constexpr int kLaShort = 16;
+cudaError_t launch_la_short(const LaCall& a, LaPass pass, cudaStream_t s);
 // float32 activations, and bfloat16 ones that the other kernel does not take
 cudaError_t launch_la_split(const LaCall& a, LaPass pass, cudaStream_t s);
 // bfloat16 operands that tile copies take (widths and strides multiples of

@@ -193,7 +193,8 @@ LaArgs base_args(const La& g, const LaWork& w, int nrole, const float* ld, const
 
 // One pass of every role.
 cudaError_t launch_pass(const LaArgs& a, LaPass pass, cudaStream_t s) {
-  auto* const launch = la_mma_supported(a) ? launch_la_mma : launch_la_split;
+  // (at most kLaShort tokens are never cut into segments)
+  auto* const launch = la_mma_supported(a) ? launch_la_mma : a.call.L <= kLaShort ? launch_la_short : launch_la_split;
   for (int i = 0; i < a.nrole; ++i) {
     LaCall c = a.call;
     c.role = a.role[i];

@@ -120,7 +120,7 @@ DTYPES = ["fp32", "bf16"]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("L", [1, 2, 31, 32, 33, 127, 128, 129, 300])
+@pytest.mark.parametrize("L", [1, 2, 16, 17, 31, 32, 33, 127, 128, 129, 300])
 def test_lengths(dtype, L):
     Problem(2, L, 3, 0, 64, 128, dtype, states=L % 2 == 1, seed=L).check()
 
@@ -130,6 +130,13 @@ def test_lengths(dtype, L):
                                  (8, 120), (72, 8), (127, 128), (100, 4)])
 def test_widths(dtype, P, N):
     Problem(2, 150, 2, 0, P, N, dtype, states=True, seed=P * 200 + N).check()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("P,N,lens", [(128, 96, [12, 0, 3]), (37, 53, [1, 16]), (1, 1, [2]),
+                                      (64, 128, [16] * 200)])
+def test_short_sequences(dtype, P, N, lens):
+    Problem(len(lens), 16, 4, 2, P, N, dtype, lens=lens, states=True, seed=P).check()
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
