@@ -405,7 +405,7 @@ int m3_mimo_step(const m3_ssm_config* cfg, const float* c, const float* b, const
 enum m3_dtype { M3_DTYPE_FP32 = 0, M3_DTYPE_BF16 = 1 };
 
 /* Shape of m3_qk_norm_rope: `rows` tokens with num_q_heads query heads and
- * num_k_heads key heads (either may be 0) of head_dim values, 1 <= head_dim <=
+ * num_k_heads key heads (at most 65535, either may be 0) of head_dim values, 1 <= head_dim <=
  * 256; num_rope_angles A, 2A <= head_dim; tables of max_positions rows. A row
  * of an operand starts *_stride elements after the one before it (0: dense,
  * heads * head_dim), so queries and keys can be columns of a packed
@@ -471,7 +471,7 @@ int m3_qk_norm_rope_backward(const m3_qk_norm_rope_config* cfg, const void* q, c
 /* Shape of linear attention: batch_size sequences of up to sequence_length
  * tokens in total_rows rows; num_heads H with values of head_dim P, queries
  * and keys of state_size N shared by the H / G heads of each of num_groups G
- * groups (0: one per head), 1 <= P, N <= 128. Row strides in elements as in
+ * groups (0: one per head), 1 <= P, N <= 128, B H <= 2^22. Row strides in elements as in
  * m3_qk_norm_rope_config (0: dense). scale multiplies every output. num_slots
  * is read by the step only. */
 typedef struct {

@@ -531,6 +531,27 @@ def test_calls_captured_into_a_graph_replay_to_the_same_bits():
     assert torch.equal(out, want) and torch.equal(fin, want_fin)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_adjoints_captured_into_a_graph_replay_to_the_same_bits(dtype):
+    """The three roles run beside each other by programmatic launches, which a graph keeps."""
+    import torch
+    p = Problem(1, 2100, 4, 2, 64, 128, dtype, states=True, seed=23)  # cut into segments
+    want = p.backward()
+    grads = [torch.empty_like(p.d[x]) for x in "qkv"]
+    g0 = torch.empty_like(p.s0)
+    ws = ws_of(m3.m3_linear_attention_backward_workspace(p.cfg))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m3.m3_linear_attention_backward(p.cfg, p.d["do"], p.d["q"], p.d["k"], p.d["v"], p.ld, None,
+                                        p.s0, p.ds, *grads, g0, ws)
+    for _ in range(2):
+        for t in (*grads, g0):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*grads, g0), want))
+
+
 def test_the_example_runs():
     import importlib.util
     import os
