@@ -8,7 +8,8 @@
 // are in shared memory as float32. Bound by its instructions, some 25 a row, token and
 // warp, so it serves few tokens: 13 float32 sequences of 12 tokens, 32 heads of
 // 128 x 96, take 36 us and of 16 tokens 46 us, where the chunked kernel takes 61 us for
-// 12 as for 40; four sequences of two tokens and one head 3.9 us.
+// 12 as for 40; four sequences of two tokens and one head 3.9 us. Small bfloat16 calls
+// come here too, where the tensor-core kernel's one chunk takes 7 us.
 #include "linattn.cuh"
 
 namespace m3 {
@@ -20,7 +21,7 @@ constexpr int kRows = 4;  // state rows a lane group takes at once
 template <typename T>
 __global__ void __launch_bounds__(kThreads) k_la_short(const __grid_constant__ LaCall a, int lpr, int rows_per_block) {
   __shared__ __align__(16) float sq[kLaShort][128], sk[kLaShort][128], sv[kLaShort][128];
-  if (a.clear && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicExch(a.status, 0u);
+  la_begin(a);
   const LaRole& r = a.role;
   const int bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
   const int N = r.N, P = r.P;
@@ -107,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) k_la_short(const __grid_constant__ L
       }
     }
   }
+  la_end(a);
 }
 
 }  // namespace
@@ -122,10 +124,9 @@ cudaError_t launch_la_short(const LaCall& a, LaPass, cudaStream_t s) {
   int per = (int)((want + round - 1) / round) * round;
   if (per > a.role.P) per = a.role.P;
   const dim3 grid((unsigned)bh, (unsigned)((a.role.P + per - 1) / per));
-  if (a.dtype == M3_DTYPE_FP32) k_la_short<float><<<grid, kThreads, 0, s>>>(a, lpr, per);
-  else k_la_short<__nv_bfloat16><<<grid, kThreads, 0, s>>>(a, lpr, per);
-  count_launches(1);
-  return cudaGetLastError();
+  return a.dtype == M3_DTYPE_FP32
+             ? launch_role(k_la_short<float>, grid, kThreads, 0, a.beside, s, a, lpr, per)
+             : launch_role(k_la_short<__nv_bfloat16>, grid, kThreads, 0, a.beside, s, a, lpr, per);
 }
 
 }  // namespace m3

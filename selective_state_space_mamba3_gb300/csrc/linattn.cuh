@@ -84,7 +84,7 @@ struct LaArgs {
 };
 
 enum LaPass { kLaMain = 0, kLaSummary = 1 };
-// sequences of at most kLaShort tokens that the bfloat16 kernel does not take
+// sequences of at most kLaShort tokens
 constexpr int kLaShort = 16;
 cudaError_t launch_la_short(const LaCall& a, LaPass pass, cudaStream_t s);
 // float32 activations, and bfloat16 ones that the other kernel does not take
@@ -159,7 +159,7 @@ __device__ __forceinline__ float la_power(float ld, int64_t d) {
 // Launches a chunk kernel, beside the launch before it where that is another
 // role's pass (programmatic stream serialization).
 template <typename... Ps, typename... As>
-cudaError_t launch_role(void (*kernel)(Ps...), unsigned grid, int threads, size_t smem, bool beside,
+cudaError_t launch_role(void (*kernel)(Ps...), dim3 grid, int threads, size_t smem, bool beside,
                         cudaStream_t s, const As&... args) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
@@ -167,7 +167,7 @@ cudaError_t launch_role(void (*kernel)(Ps...), unsigned grid, int threads, size_
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

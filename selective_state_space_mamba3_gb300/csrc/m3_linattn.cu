@@ -193,8 +193,14 @@ LaArgs base_args(const La& g, const LaWork& w, int nrole, const float* ld, const
 
 // One pass of every role.
 cudaError_t launch_pass(const LaArgs& a, LaPass pass, cudaStream_t s) {
-  // (at most kLaShort tokens are never cut into segments)
-  auto* const launch = la_mma_supported(a) ? launch_la_mma : a.call.L <= kLaShort ? launch_la_short : launch_la_split;
+  // A few tokens (never cut into segments) go one by one: up to kLaShort where the
+  // float32 kernel would take them; up to eight, and to the work that costs what the
+  // bfloat16 kernel's one chunk does (7 us; 0.56 us for a million of B H L P N), where
+  // that one would. Their outputs have one rounding only.
+  const bool tiles = la_mma_supported(a);
+  const double work = (double)a.call.B * a.call.H * a.call.L * a.role[0].P * a.role[0].N;
+  const bool few = tiles ? a.call.L <= 8 && work <= 8e6 : a.call.L <= kLaShort;
+  auto* const launch = few ? launch_la_short : tiles ? launch_la_mma : launch_la_split;
   for (int i = 0; i < a.nrole; ++i) {
     LaCall c = a.call;
     c.role = a.role[i];
