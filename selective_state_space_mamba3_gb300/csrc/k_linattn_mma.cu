@@ -6,7 +6,7 @@
 // j' counted in walking order, and S [N][64] the state:
 //   A    = Q K^T                      [128 x 128]        tensor cores
 //   Oi   = Q S                        [128 x 64]         tensor cores
-//   P    = intra (A o w)              to bfloat16, kept in tensor memory (mild decays: less its row factor)
+//   P    = intra (A o w)              to bfloat16, kept in tensor memory
 //   out  = inter lam^(i'+1) Oi + P V  [128 x 64]         tensor cores (P from tensor memory)
 //   S'   = lam^n S + K^T V^           V^_j = kv lam^(n-1-j') V_j
 // Rounding: P and the S that multiplies Q go to bfloat16, like the output
@@ -28,8 +28,8 @@
 // The floor is HBM's: 2 (2 N + 2 P) bytes a token and head, 4,200 cycles a chunk and
 // SM at N = 128, P = 64; the products take about 2,600 (a step of 128 x 64 x 16 as
 // long as one of 128 x 128 x 16), the threads' instructions about 2,000. Measured on
-// prompts of 8 x 2048 tokens, 32 heads, P 64, N 128: 75 us, 5.3 TB/s, 79 % of a copy's
-// rate; adjoints of the same 262 us. With few blocks a chunk's own chain binds, some
+// prompts of 8 x 2048 tokens, 32 heads, P 64, N 128: 76 us, 5.3 TB/s, 78 % of a copy's
+// rate; adjoints of the same 267 us. With few blocks a chunk's own chain binds, some
 // 7,000 cycles alone on an SM.
 //
 // A chunk of n < 128 tokens (a sequence's end) zeroes its K and V rows up to a
@@ -170,18 +170,13 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
   const int64_t sbase = (int64_t)bh * N * P;
   // chunk c of a row is at the first one's address with c's bits flipped in
   const uint32_t at_state = base + chunk_at(srow, scol / 8);
-  // the state that multiplies Q; `f`: MILD, what is common to the chunk's rows
-  auto put_state = [&](float f) {
-    float x[SC];
-#pragma unroll
-    for (int j = 0; j < SC; j += 2) set(x, j, MILD ? __fmul2_rn(make_float2(f, f), pair(st, j)) : pair(st, j));
+  auto put_state = [&]() {  // the state that multiplies Q
 #pragma unroll
     for (int c = 0; c < SC / 8; ++c)
       sts<kS>(at_state ^ (c << 4),
-              make_uint4(pack(x[8 * c], x[8 * c + 1]), pack(x[8 * c + 2], x[8 * c + 3]),
-                         pack(x[8 * c + 4], x[8 * c + 5]), pack(x[8 * c + 6], x[8 * c + 7])));
+              make_uint4(pack(st[8 * c], st[8 * c + 1]), pack(st[8 * c + 2], st[8 * c + 3]),
+                         pack(st[8 * c + 4], st[8 * c + 5]), pack(st[8 * c + 6], st[8 * c + 7])));
   };
-  const float ratio = MILD ? r.inter / r.intra : 1.f;
   if (warp < kWarps) {
 #pragma unroll
     for (int j = 0; j < SC; ++j) {
@@ -192,10 +187,7 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
         else if (r.init) st[j] = r.init[sbase + (int64_t)p * r.sp + (int64_t)srow * r.sn];
       }
     }
-    if (!SUMMARY)
-      put_state(ratio * (!MILD ? 1.f
-                         : !rev ? la_power(ld, kC / 2 + 1)
-                                : expf(ld * (float)(min(kC, ntok - (nchunk - 1) * kC) - (first ? r.shift : 0) - kC / 2))));
+    if (!SUMMARY) put_state();
   }
   tc::fence_async_smem();
   __syncthreads();
@@ -337,18 +329,23 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
     const int i = 32 * quad + lane;  // this thread's row of A, P and O
     const uint32_t at_v = base + chunk_at(tid >> 2, 2 * (tid & 3)), at_o = base + chunk_at(i, 2 * grp);
     // A decay of at most e^0.5 a token splits into a factor of the row and one of the
-    // column over the whole chunk, lam^(i-j) = lam^(i-64) lam^(64-j), each within
-    // e^32 (which leaves scores times values 10^24): P takes the column's alone, S
-    // the one its readout shares, and the row's is the output's. Stronger decays
-    // take a row factor for every block of 16 columns, and lam^d from the table on
-    // the diagonal.
+    // column over the whole chunk, lam^(i-j) = lam^(i-64) lam^(64-j), each within e^32
+    // and multiplied with each other before the score, so that no term is larger than
+    // its result or lost below it. (With the row's factor left to the output, and the
+    // readout's in S, calls take 1 to 3 % less time, but scores times values above
+    // 10^24 overflow and results below 10^-24 lose their bits.) Stronger decays take
+    // a row factor for every block of 16 columns, and lam^d from the table on the
+    // diagonal: the layer's prompts 84 us instead of 76, its adjoints 304 instead of 267.
     const float intra = r.intra;
-    const float rowf = MILD ? intra * expf(ld * (float)(rev ? kC / 2 - i : i - kC / 2)) : 1.f;
     float fac[2];
+    if (MILD) {
+      fac[0] = fac[1] = intra * expf(ld * (float)(rev ? kC / 2 - i : i - kC / 2));
+    } else {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int c = 32 * grp + 16 * x, d = rev ? c - i : i - c - 15;
-      fac[x] = MILD || d < 0 ? 0.f : intra * power(d);
+      for (int x = 0; x < 2; ++x) {
+        const int c = 32 * grp + 16 * x, d = rev ? c - i : i - c - 15;
+        fac[x] = d < 0 ? 0.f : intra * power(d);
+      }
     }
     for (int ci = 0; ci < nchunk; ++ci) {
       const uint32_t ph = ci & 1;
@@ -365,6 +362,7 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
         arrive(kBarZ);
         if (!wait(kBarZ, 0)) break;
       }
+      uint32_t oi[16];
       // V^: the high part to X, the rest to the Q tile once A and Oi are done
       if (!wait(kBarV, ph)) break;
       {
@@ -390,6 +388,7 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
         if (!SUMMARY) {
           if (!wait(kBarA, ph)) break;
           tc::fence_after();
+          ld16(tw + kColO + 16 * grp, oi);  // while V^ is stored
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) sts<kQ>(at_v ^ (c << 4), low[c]);
@@ -412,6 +411,15 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
         arrive(kBarW);
       }
       if (!SUMMARY) {
+        {  // Oi scaled in place, for O to be added
+          const float f = r.inter * power(max(rev ? n - 1 - i : i, 0) + 1 - shift);
+          float o[16];
+          wait_ld16(oi);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2)
+            set(o, e, __fmul2_rn(make_float2(f, f), make_float2(__uint_as_float(oi[e]), __uint_as_float(oi[e + 1]))));
+          tc::tmem_st16_async(tw + kColO + 16 * grp, o);
+        }
         // P: columns 32 grp .. in blocks of 16, over the columns of A already read
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -427,16 +435,8 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
 #pragma unroll
               for (int e = 0; e < 16; e += 4) {
                 const float4 w = *reinterpret_cast<const float4*>(&sm.col[(MILD ? c : 0) + e]);
-                float2 u = __fmul2_rn(make_float2(s[e], s[e + 1]), make_float2(w.x, w.y));
-                float2 v = __fmul2_rn(make_float2(s[e + 2], s[e + 3]), make_float2(w.z, w.w));
-                if (!MILD) {
-                  u = __fmul2_rn(u, f2);
-                  v = __fmul2_rn(v, f2);
-                }
-                s[e] = u.x;
-                s[e + 1] = u.y;
-                s[e + 2] = v.x;
-                s[e + 3] = v.y;
+                set(s, e, __fmul2_rn(pair(s, e), __fmul2_rn(make_float2(w.x, w.y), f2)));
+                set(s, e + 2, __fmul2_rn(pair(s, e + 2), __fmul2_rn(make_float2(w.z, w.w), f2)));
               }
             }
             if (!full) {
@@ -454,16 +454,6 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
             for (int e = 0; e < 8; ++e) pk[e] = pack(s[2 * e], s[2 * e + 1]);
           }
           st8(tw + 32 * grp + 8 * x, pk);
-        }
-        if (!MILD) {  // Oi scaled in place, for O to be added
-          const int at = max(rev ? n - 1 - i : i, 0);
-          const float f = r.inter * power(at + 1 - shift);
-          float o[16];
-          ld16(tw + kColO + 16 * grp, o);
-          tc::tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] *= f;
-          tc::tmem_st16_async(tw + kColO + 16 * grp, o);
         }
         tc::tmem_wait_st();
         tc::fence_before();
@@ -483,7 +473,7 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
 #pragma unroll
         for (int j = 0; j < SC; j += 2)
           set(st, j, __ffma2_rn(make_float2(dec, dec), pair(st, j), pair(kv, j)));
-        if (!SUMMARY) put_state(ratio * power(rev ? kC / 2 : kC / 2 + 1));
+        if (!SUMMARY) put_state();
       }
       tc::fence_before();
       tc::fence_async_smem();
@@ -497,10 +487,6 @@ __device__ __forceinline__ void walk(const LaCall& a, const Maps& maps, int pt, 
         tc::tmem_wait_ld();
         tc::fence_before();
         arrive(kBarE);
-        if (MILD) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) set(o, e, __fmul2_rn(make_float2(rowf, rowf), pair(o, e)));
-        }
         const int64_t at_out = (chunk_row(ci) + i) * r.os + (int64_t)h * P + p_lo + c0;
         if (r.out_rep > 1) {  // float32 partials of a shared head
           if (i < n) {
@@ -552,8 +538,9 @@ __global__ void __launch_bounds__(kThreads, 2)
   la_begin(a);
   const int tiles = (a.role.P + 63) / 64, item = blockIdx.x % tiles, unit = blockIdx.x / tiles;
   const int bh = unit % (a.B * a.H), seg = unit / (a.B * a.H);
-  const float ld = a.log_decay[bh % a.H], ratio = a.role.inter / a.role.intra;
-  const bool mild = fabsf(ld) <= 0.5f && fabsf(ratio) < 1e6f && fabsf(ratio) > 1e-6f;  // else: strong, or scale 0
+  // (the scale is in the row factors, within e^32)
+  const float scale = fabsf(a.role.intra);
+  const bool mild = fabsf(a.log_decay[bh % a.H]) <= 0.5f && scale < 1e6f && scale > 1e-6f;  // else: strong, or scale 0
   if (mild && !SUMMARY) walk<NB, SUMMARY, true>(a, maps, item, bh, seg, raw);
   else walk<NB, SUMMARY, false>(a, maps, item, bh, seg, raw);
   la_end(a);

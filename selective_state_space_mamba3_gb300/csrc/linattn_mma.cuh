@@ -36,16 +36,27 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t a_step, 
 }
 
 // 16 columns of this warp's 32 lanes, no wait.
-__device__ __forceinline__ void ld16(uint32_t addr, float* v) {
-  uint32_t r[16];
+__device__ __forceinline__ void ld16(uint32_t addr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
+}
+__device__ __forceinline__ void ld16(uint32_t addr, float* v) {
+  uint32_t r[16];
+  ld16(addr, r);
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+// Waits for a load that other work stands behind: the registers pass through the
+// statement, so that nothing touches them before it.
+__device__ __forceinline__ void wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 __device__ __forceinline__ void ld8(uint32_t addr, float* v) {
   uint32_t r[8];
