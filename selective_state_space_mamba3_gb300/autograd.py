@@ -154,20 +154,21 @@ class _QkNormRope(torch.autograd.Function):
         outs = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
                 for t in (q, k)]
         m3.m3_qk_norm_rope(cfg, q, k, q_weight, k_weight, cos, sin, positions, *outs)
-        ctx.cfg, ctx.tables = cfg, (cos, sin, positions)
-        ctx.save_for_backward(q, k, q_weight, k_weight)
+        ctx.cfg = cfg
+        # the tables too: one that is written again before the backward call is an error
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
         return tuple(outs)
 
     @staticmethod
     def backward(ctx, *grads):
-        q, k, wq, wk = ctx.saved_tensors
+        q, k, wq, wk, *tables = ctx.saved_tensors
         some = q if q is not None else k
         dy = [None if t is None else torch.zeros(t.shape, dtype=t.dtype, device=t.device)
               if g is None else g.contiguous() for t, g in zip((q, k), grads)]
         dx = [None if g is None else torch.empty_like(g) for g in dy]
         dw = [None if w is None else torch.empty_like(w) for w in (wq, wk)]
         ws = _workspace(m3.m3_qk_norm_rope_backward_workspace(ctx.cfg), some)
-        m3.m3_qk_norm_rope_backward(ctx.cfg, q, k, wq, wk, *ctx.tables, *dy, *dx, *dw, ws)
+        m3.m3_qk_norm_rope_backward(ctx.cfg, q, k, wq, wk, *tables, *dy, *dx, *dw, ws)
         return (None,) * 6 + (*dx, *dw)
 
 
@@ -197,21 +198,21 @@ class _LinearAttention(torch.autograd.Function):
             final = torch.empty(batch_size, v.shape[-2], v.shape[-1], q.shape[-1], device=v.device)
         ws = _workspace(m3.m3_linear_attention_forward_workspace(cfg), v)
         m3.m3_linear_attention_forward(cfg, q, k, v, log_decay, offsets, initial_state, out, final, ws)
-        ctx.cfg, ctx.offsets = cfg, offsets
-        ctx.save_for_backward(log_decay, q, k, v, initial_state)
+        ctx.cfg = cfg
+        ctx.save_for_backward(log_decay, offsets, q, k, v, initial_state)
         return out, final
 
     @staticmethod
     def backward(ctx, grad_out, grad_final):
-        log_decay, q, k, v, initial = ctx.saved_tensors
-        new = torch.empty if ctx.offsets is None else torch.zeros
+        log_decay, offsets, q, k, v, initial = ctx.saved_tensors
+        new = torch.empty if offsets is None else torch.zeros
         if grad_out is None:
             grad_out = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
         grads = [new(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
         d_init = None if initial is None else torch.empty_like(initial)
         ws = _workspace(m3.m3_linear_attention_backward_workspace(ctx.cfg), v)
         m3.m3_linear_attention_backward(
-            ctx.cfg, grad_out.contiguous(), q, k, v, log_decay, ctx.offsets, initial,
+            ctx.cfg, grad_out.contiguous(), q, k, v, log_decay, offsets, initial,
             None if grad_final is None else grad_final.contiguous(), *grads, d_init, ws)
         return (None,) * 7 + (*grads, d_init)
 

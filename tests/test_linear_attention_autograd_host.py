@@ -1,0 +1,64 @@
+"""The autograd bindings of the linear-attention operators without a GPU: the library's
+calls are replaced by recorders, everything around them runs as it is."""
+import pytest
+import torch
+
+from selective_state_space_mamba3_gb300 import autograd
+
+ROWS, HEADS, WIDTH, ANGLES = 6, 2, 8, 4
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The library calls made: (name, positional arguments)."""
+    made = []
+    for name in ("m3_qk_norm_rope", "m3_qk_norm_rope_backward", "m3_linear_attention_forward",
+                 "m3_linear_attention_backward"):
+        monkeypatch.setattr(autograd.m3, name, lambda *a, n=name: made.append((n, a)))
+    for name in ("m3_qk_norm_rope_backward_workspace", "m3_linear_attention_forward_workspace",
+                 "m3_linear_attention_backward_workspace"):
+        monkeypatch.setattr(autograd.m3, name, lambda cfg: 256)
+    return made
+
+
+def operand(*shape):
+    return torch.zeros(*shape or (ROWS, HEADS, WIDTH)).requires_grad_()
+
+
+def tables():
+    return torch.ones(16, ANGLES), torch.zeros(16, ANGLES), torch.zeros(ROWS, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_tables_written_again_before_the_backward_call_are_an_error(calls, which):
+    tabs = tables()
+    q, k = autograd.qk_norm_rope(operand(), operand(), None, None, *tabs, ANGLES)
+    tabs[which].add_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        (q.sum() + k.sum()).backward()
+    assert [n for n, _ in calls] == ["m3_qk_norm_rope"]
+
+
+@pytest.mark.parametrize("which", ["offsets", "log_decay", "initial_state"])
+def test_offsets_and_states_written_again_before_the_backward_call_are_an_error(calls, which):
+    t = dict(offsets=torch.tensor([0, 2, 6], dtype=torch.int32), log_decay=torch.zeros(HEADS),
+             initial_state=torch.zeros(2, HEADS, WIDTH, WIDTH))
+    out = autograd.linear_attention(operand(), operand(), operand(), t["log_decay"], 2, 4,
+                                    offsets=t["offsets"], initial_state=t["initial_state"])
+    t[which].add_(1)
+    with pytest.raises(RuntimeError, match="inplace"):
+        out.sum().backward()
+    assert [n for n, _ in calls] == ["m3_linear_attention_forward"]
+
+
+def test_the_adjoints_get_the_forward_calls_operands(calls):
+    tabs = tables()
+    off = torch.tensor([0, 2, 6], dtype=torch.int32)
+    q, k = autograd.qk_norm_rope(operand(), operand(), None, None, *tabs, ANGLES)
+    autograd.linear_attention(q, k, operand(), torch.zeros(HEADS), 2, 4, offsets=off).sum().backward()
+    assert [n for n, _ in calls] == ["m3_qk_norm_rope", "m3_linear_attention_forward",
+                                     "m3_linear_attention_backward", "m3_qk_norm_rope_backward"]
+    fwd, bwd = calls[1][1], calls[2][1]
+    assert torch.equal(fwd[5], off) and torch.equal(bwd[6], off)
+    for a, b in zip(calls[0][1][5:8], calls[3][1][5:8]):
+        assert torch.equal(a, b)
