@@ -157,6 +157,7 @@ class _QkNormRope(torch.autograd.Function):
         ctx.cfg = cfg
         # the tables too: one that is written again before the backward call is an error
         ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.set_materialize_grads(False)
         return tuple(outs)
 
     @staticmethod
@@ -200,6 +201,7 @@ class _LinearAttention(torch.autograd.Function):
         m3.m3_linear_attention_forward(cfg, q, k, v, log_decay, offsets, initial_state, out, final, ws)
         ctx.cfg = cfg
         ctx.save_for_backward(log_decay, offsets, q, k, v, initial_state)
+        ctx.set_materialize_grads(False)  # an unused final state is a NULL gradient, not zeros to read
         return out, final
 
     @staticmethod

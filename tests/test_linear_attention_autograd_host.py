@@ -62,3 +62,26 @@ def test_the_adjoints_get_the_forward_calls_operands(calls):
     assert torch.equal(fwd[5], off) and torch.equal(bwd[6], off)
     for a, b in zip(calls[0][1][5:8], calls[3][1][5:8]):
         assert torch.equal(a, b)
+
+
+def test_an_unused_state_costs_the_adjoint_no_zeros(calls):
+    out, fin = autograd.linear_attention(operand(), operand(), operand(), torch.zeros(HEADS), 1, ROWS,
+                                         return_state=True)
+    out.sum().backward()
+    grad_out, grad_final = calls[1][1][1], calls[1][1][8]
+    assert grad_out is not None and grad_final is None
+
+
+def test_outputs_the_loss_does_not_use_have_zero_gradients(calls):
+    v = operand()
+    _, fin = autograd.linear_attention(operand(), operand(), v, torch.zeros(HEADS), 1, ROWS,
+                                       return_state=True)
+    fin.sum().backward()
+    grad_out, grad_final = calls[1][1][1], calls[1][1][8]
+    assert torch.equal(grad_out, torch.zeros_like(v)) and torch.equal(grad_final, torch.ones_like(fin))
+    del calls[:]
+    q, _ = autograd.qk_norm_rope(operand(), operand(ROWS, 1, WIDTH), None, None, *tables(), ANGLES)
+    q.sum().backward()
+    dq, dk = calls[1][1][8:10]
+    assert torch.equal(dq, torch.ones(ROWS, HEADS, WIDTH))
+    assert torch.equal(dk, torch.zeros(ROWS, 1, WIDTH))
