@@ -176,7 +176,10 @@ class _QkNormRope(torch.autograd.Function):
 def qk_norm_rope(q, k, q_weight, k_weight, cos_table, sin_table, positions, num_rope_angles,
                  epsilon=1e-6):
     """Norm and rotation of query and key heads (m3_qk_norm_rope) with its adjoint:
-    the normalised, rotated q and k, dense. q or k, and each weight, may be None."""
+    the normalised, rotated q and k, dense. q or k, and each weight, may be None. The
+    rotation is fixed: its tables get no gradient."""
+    if any(t is not None and t.requires_grad for t in (cos_table, sin_table)):
+        raise ValueError("the rotation is fixed: its tables get no gradient")
     rows = 0 if cos_table is None else cos_table.shape[0]
     return _QkNormRope.apply(num_rope_angles, rows, epsilon, cos_table, sin_table, positions, q, k,
                              q_weight, k_weight)

@@ -85,3 +85,12 @@ def test_outputs_the_loss_does_not_use_have_zero_gradients(calls):
     dq, dk = calls[1][1][8:10]
     assert torch.equal(dq, torch.ones(ROWS, HEADS, WIDTH))
     assert torch.equal(dk, torch.zeros(ROWS, 1, WIDTH))
+
+
+@pytest.mark.parametrize("which", [0, 1])
+def test_a_gradient_of_the_rotation_tables_is_refused(calls, which):
+    tabs = tables()
+    tabs[which].requires_grad_()
+    with pytest.raises(ValueError, match="tables"):
+        autograd.qk_norm_rope(operand(), operand(), None, None, *tabs, ANGLES)
+    assert not calls
