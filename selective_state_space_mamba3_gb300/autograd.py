@@ -32,6 +32,7 @@ the C ABI's layout; angle may be None when num_rope_angles is 0.
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as m3
 
@@ -161,6 +162,7 @@ class _QkNormRope(torch.autograd.Function):
         return tuple(outs)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         q, k, wq, wk, *tables = ctx.saved_tensors
         some = q if q is not None else k
@@ -208,6 +210,7 @@ class _LinearAttention(torch.autograd.Function):
         return out, final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_out, grad_final):
         log_decay, offsets, q, k, v, initial = ctx.saved_tensors
         new = torch.empty if offsets is None else torch.zeros

@@ -94,3 +94,16 @@ def test_a_gradient_of_the_rotation_tables_is_refused(calls, which):
     with pytest.raises(ValueError, match="tables"):
         autograd.qk_norm_rope(operand(), operand(), None, None, *tabs, ANGLES)
     assert not calls
+
+
+def test_a_second_derivative_is_refused(calls):
+    """The adjoints are no functions of torch: a graph of them would lack their terms."""
+    x = operand()
+    q, _ = autograd.qk_norm_rope(x, None, None, None, *tables(), ANGLES)
+    (g,) = torch.autograd.grad(q.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
+    out = autograd.linear_attention(x, x, x, torch.zeros(HEADS), 1, ROWS)
+    (g,) = torch.autograd.grad(out.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
