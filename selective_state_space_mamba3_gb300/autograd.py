@@ -32,7 +32,6 @@ the C ABI's layout; angle may be None when num_rope_angles is 0.
 from __future__ import annotations
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import _binding as m3
 
@@ -146,6 +145,30 @@ def mimo_scan(cfg, c, b, x, z, adt, dt, trap, angle, c_bias, b_bias, d, mimo_x, 
                            b_bias, d, mimo_x, mimo_z, mimo_o, norm_weight)
 
 
+class _NoDerivative(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, grad):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, grad):
+        raise RuntimeError("the adjoints of the linear-attention operators are once_differentiable: "
+                           "they have no derivative themselves")
+
+
+def _once_differentiable(backward):
+    """Gradients made with create_graph=True carry a graph that raises. (torch's own mark
+    of this name leaves it out where the incoming gradients need none, though the operands'
+    gradients depend on the operands all the same.)"""
+    def once(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        return tuple(None if g is None else _NoDerivative.apply(g.requires_grad_()) for g in out)
+    return once
+
+
 class _QkNormRope(torch.autograd.Function):
     @staticmethod
     def forward(ctx, num_rope_angles, max_positions, epsilon, cos, sin, positions, q, k, q_weight,
@@ -162,7 +185,7 @@ class _QkNormRope(torch.autograd.Function):
         return tuple(outs)
 
     @staticmethod
-    @once_differentiable
+    @_once_differentiable
     def backward(ctx, *grads):
         q, k, wq, wk, *tables = ctx.saved_tensors
         some = q if q is not None else k
@@ -210,7 +233,7 @@ class _LinearAttention(torch.autograd.Function):
         return out, final
 
     @staticmethod
-    @once_differentiable
+    @_once_differentiable
     def backward(ctx, grad_out, grad_final):
         log_decay, offsets, q, k, v, initial = ctx.saved_tensors
         new = torch.empty if offsets is None else torch.zeros

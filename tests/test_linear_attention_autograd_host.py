@@ -107,3 +107,14 @@ def test_a_second_derivative_is_refused(calls):
     (g,) = torch.autograd.grad(out.sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.sum().backward()
+
+
+def test_a_second_derivative_among_other_terms_is_refused(calls):
+    x = operand()
+    for loss in (lambda y: y.sum(), lambda y: y.square().sum()):
+        out = autograd.linear_attention(x, x, x, torch.zeros(HEADS), 1, ROWS)
+        (g,) = torch.autograd.grad(loss(out), x, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (g.square().sum() + x.square().sum()).backward()
+        (g,) = torch.autograd.grad(loss(autograd.linear_attention(x, x, x, torch.zeros(HEADS), 1, ROWS)), x)
+        assert not g.requires_grad
