@@ -224,7 +224,8 @@ class _LinearAttention(torch.autograd.Function):
         out = new(v.shape, dtype=v.dtype, device=v.device)
         final = None
         if want_state:
-            final = torch.empty(batch_size, v.shape[-2], v.shape[-1], q.shape[-1], device=v.device)
+            final = torch.empty(batch_size, v.shape[-2], v.shape[-1], q.shape[-1],
+                                dtype=torch.float32, device=v.device)
         ws = _workspace(m3.m3_linear_attention_forward_workspace(cfg), v)
         m3.m3_linear_attention_forward(cfg, q, k, v, log_decay, offsets, initial_state, out, final, ws)
         ctx.cfg = cfg

@@ -118,3 +118,15 @@ def test_a_second_derivative_among_other_terms_is_refused(calls):
             (g.square().sum() + x.square().sum()).backward()
         (g,) = torch.autograd.grad(loss(autograd.linear_attention(x, x, x, torch.zeros(HEADS), 1, ROWS)), x)
         assert not g.requires_grad
+
+
+@pytest.mark.parametrize("default", [torch.float64, torch.bfloat16])
+def test_states_are_float32_whatever_the_default_type(calls, default):
+    x = operand()  # float32
+    torch.set_default_dtype(default)
+    try:
+        out, fin = autograd.linear_attention(x, x, x, torch.zeros(HEADS, dtype=torch.float32), 1, ROWS,
+                                             return_state=True)
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert out.dtype == fin.dtype == torch.float32
