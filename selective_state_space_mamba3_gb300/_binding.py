@@ -421,21 +421,48 @@ _types = None
 
 
 def _torch_types():
-    """(float32, bfloat16, int32, the raw handle of a device's current stream)."""
+    """(float32, bfloat16, int32, the raw handle of a device's current stream, the current device)."""
     global _types
     if _types is None:
         import torch
         _types = (torch.float32, torch.bfloat16, torch.int32,
                   getattr(torch._C, "_cuda_getCurrentRawStream", None) or
-                  (lambda i: torch.cuda.current_stream(i).cuda_stream))
+                  (lambda i: torch.cuda.current_stream(i).cuda_stream),
+                  getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
     return _types
 
 
-def _stream_of(stream, t):
-    """The given stream, or the current one of the device that holds t."""
+def _device_of(t):
+    """The device of a call, from one of its operands: the library launches on the calling
+    thread's current device, so it has to be that one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise TypeError("activations must be CUDA tensors")
+    current = _torch_types()[4]()
+    if dev != current:
+        raise ValueError(f"operands on cuda:{dev}, but the current device is cuda:{current}")
+    return dev
+
+
+def _other_device(t, dev):
+    return ValueError(f"operands on different devices: cuda:{t.get_device()} and cuda:{dev}")
+
+
+def _stream_of(stream, dev):
+    """The given stream, or the device's current one."""
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    return _torch_types()[3](t.device.index)
+    return _torch_types()[3](dev)
+
+
+def _ws_on(workspace, dev):
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev:
+        if workspace.get_device() < 0:
+            raise TypeError("the workspace must be a CUDA tensor")
+        raise _other_device(workspace, dev)
+    return _ws(workspace)
 
 
 def _row_stride(t):
@@ -468,14 +495,16 @@ def _dtype(t):
     raise TypeError("activations must be float32 or bfloat16")
 
 
-def _act(t, dtype, rows, heads, width, stride):
+def _act(t, dtype, rows, heads, width, stride, dev):
     """Device pointer of an activation; its shape and stride must be the config's."""
     stride = stride or heads * width
-    if (t.dtype is dtype and t.is_cuda and rows and t.shape == (rows, heads, width) and
+    if (t.dtype is dtype and t.get_device() == dev and rows and t.shape == (rows, heads, width) and
             t.stride() == (stride, width, 1)):
         return t.data_ptr()
     if not t.is_cuda or t.dtype != dtype:
         raise TypeError("activations must be CUDA tensors of the config's type")
+    if t.get_device() != dev:
+        raise _other_device(t, dev)
     n = t.numel()
     if tuple(t.shape[-2:]) != (heads, width) or n != rows * heads * width:
         raise ValueError(f"expected {rows} rows of [{heads}, {width}], got {tuple(t.shape)}")
@@ -484,12 +513,14 @@ def _act(t, dtype, rows, heads, width, stride):
     return t.data_ptr() if n > 0 else None
 
 
-def _dense(t, dtype, shape):
+def _dense(t, dtype, shape, dev):
     """Device pointer of a dense operand of one type and shape (None passes NULL)."""
     if t is None:
         return None
-    if not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
-        raise TypeError(f"expected a contiguous {dtype} CUDA tensor")
+    if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous()):
+        if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+            raise TypeError(f"expected a contiguous {dtype} CUDA tensor")
+        raise _other_device(t, dev)
     if t.shape != shape:
         n = 1
         for x in shape:
@@ -513,29 +544,30 @@ def qk_norm_rope_config(q, k, *, num_rope_angles, max_positions=0, epsilon=1e-6,
                             num_rope_angles, max_positions, *strides, epsilon, _dtype(some))
 
 
-def _rope_operands(cfg, dtype, q, k, q_stride, k_stride):
+def _rope_operands(cfg, dtype, q, k, q_stride, k_stride, dev):
     rows, d, hq, hk = cfg.rows, cfg.head_dim, cfg.num_q_heads, cfg.num_k_heads
-    return (_act(q, dtype, rows, hq, d, q_stride) if hq else None,
-            _act(k, dtype, rows, hk, d, k_stride) if hk else None)
+    return (_act(q, dtype, rows, hq, d, q_stride, dev) if hq else None,
+            _act(k, dtype, rows, hk, d, k_stride, dev) if hk else None)
 
 
-def _rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions):
-    f32, _, i32, _ = _torch_types()
+def _rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions, dev):
+    f32, _, i32 = _torch_types()[:3]
     d, a = (cfg.head_dim,), cfg.num_rope_angles
     table = (cfg.max_positions, a) if a else (0,)
-    return (_dense(q_weight, f32, d), _dense(k_weight, f32, d), _dense(cos_table, f32, table),
-            _dense(sin_table, f32, table), _dense(positions, i32, (cfg.rows,)))
+    return (_dense(q_weight, f32, d, dev), _dense(k_weight, f32, d, dev),
+            _dense(cos_table, f32, table, dev), _dense(sin_table, f32, table, dev),
+            _dense(positions, i32, (cfg.rows,), dev))
 
 
 def m3_qk_norm_rope(cfg: QkNormRopeConfig, q, k, q_weight, k_weight, cos_table, sin_table,
                     positions, q_out, k_out, stream=None):
     lib = load_library()
-    dt = _torch_types()[cfg.dtype]
+    dt, dev = _torch_types()[cfg.dtype], _device_of(k if q is None else q)
     _check(lib.m3_qk_norm_rope(
-        ctypes.byref(cfg), *_rope_operands(cfg, dt, q, k, cfg.q_stride, cfg.k_stride),
-        *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions),
-        *_rope_operands(cfg, dt, q_out, k_out, cfg.q_out_stride, cfg.k_out_stride),
-        _stream_of(stream, k if q is None else q)), "m3_qk_norm_rope")
+        ctypes.byref(cfg), *_rope_operands(cfg, dt, q, k, cfg.q_stride, cfg.k_stride, dev),
+        *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions, dev),
+        *_rope_operands(cfg, dt, q_out, k_out, cfg.q_out_stride, cfg.k_out_stride, dev),
+        _stream_of(stream, dev)), "m3_qk_norm_rope")
 
 
 def m3_qk_norm_rope_backward_workspace(cfg: QkNormRopeConfig) -> int:
@@ -548,16 +580,16 @@ def m3_qk_norm_rope_backward_workspace(cfg: QkNormRopeConfig) -> int:
 def m3_qk_norm_rope_backward(cfg: QkNormRopeConfig, q, k, q_weight, k_weight, cos_table, sin_table,
                              positions, grad_q_out, grad_k_out, grad_q, grad_k, grad_q_weight,
                              grad_k_weight, workspace=None, stream=None):
-    wp, wn = _ws(workspace)
-    types = _torch_types()
+    types, dev = _torch_types(), _device_of(k if q is None else q)
     d, dt = (cfg.head_dim,), types[cfg.dtype]
+    wp, wn = _ws_on(workspace, dev)
     _check(load_library().m3_qk_norm_rope_backward(
-        ctypes.byref(cfg), *_rope_operands(cfg, dt, q, k, cfg.q_stride, cfg.k_stride),
-        *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions),
-        *_rope_operands(cfg, dt, grad_q_out, grad_k_out, cfg.q_out_stride, cfg.k_out_stride),
-        *_rope_operands(cfg, dt, grad_q, grad_k, 0, 0), _dense(grad_q_weight, types[0], d),
-        _dense(grad_k_weight, types[0], d), wp, wn, _stream_of(stream, k if q is None else q)),
-        "m3_qk_norm_rope_backward")
+        ctypes.byref(cfg), *_rope_operands(cfg, dt, q, k, cfg.q_stride, cfg.k_stride, dev),
+        *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions, dev),
+        *_rope_operands(cfg, dt, grad_q_out, grad_k_out, cfg.q_out_stride, cfg.k_out_stride, dev),
+        *_rope_operands(cfg, dt, grad_q, grad_k, 0, 0, dev),
+        _dense(grad_q_weight, types[0], d, dev), _dense(grad_k_weight, types[0], d, dev), wp, wn,
+        _stream_of(stream, dev)), "m3_qk_norm_rope_backward")
 
 
 def linear_attention_config(q, k, v, *, batch_size, sequence_length, num_heads=None, num_groups=0,
@@ -573,25 +605,29 @@ def linear_attention_config(q, k, v, *, batch_size, sequence_length, num_heads=N
 
 class _LaShapes:
     """Checks of one call's operands against its config."""
-    __slots__ = ("dt", "f32", "i32", "b", "r", "h", "g", "n", "p")
+    __slots__ = ("dev", "dt", "f32", "i32", "b", "r", "h", "g", "n", "p")
 
-    def __init__(self, cfg):
+    def __init__(self, cfg, v):
         types = _torch_types()
+        self.dev = _device_of(v)
         self.f32, self.i32, self.dt = types[0], types[2], types[cfg.dtype]
         self.b, self.r, self.h = cfg.batch_size, cfg.total_rows, cfg.num_heads
         self.g, self.n, self.p = cfg.num_groups or self.h, cfg.state_size, cfg.head_dim
 
     def qk(self, t, stride):
-        return _act(t, self.dt, self.r, self.g, self.n, stride)
+        return _act(t, self.dt, self.r, self.g, self.n, stride, self.dev)
 
     def vo(self, t, stride):
-        return _act(t, self.dt, self.r, self.h, self.p, stride)
+        return _act(t, self.dt, self.r, self.h, self.p, stride, self.dev)
 
     def state(self, t, count):
-        return _dense(t, self.f32, (count, self.h, self.p, self.n))
+        return _dense(t, self.f32, (count, self.h, self.p, self.n), self.dev)
 
     def decay(self, t):
-        return _dense(t, self.f32, (self.h,))
+        return _dense(t, self.f32, (self.h,), self.dev)
+
+    def index(self, t, count):
+        return _dense(t, self.i32, (count,), self.dev)
 
 
 def m3_linear_attention_forward_workspace(cfg: LinearAttentionConfig) -> int:
@@ -603,22 +639,22 @@ def m3_linear_attention_forward_workspace(cfg: LinearAttentionConfig) -> int:
 
 def m3_linear_attention_forward(cfg: LinearAttentionConfig, q, k, v, log_decay, offsets,
                                 initial_state, out, final_state, workspace=None, stream=None):
-    wp, wn = _ws(workspace)
-    x = _LaShapes(cfg)
+    x = _LaShapes(cfg, v)
+    wp, wn = _ws_on(workspace, x.dev)
     _check(load_library().m3_linear_attention_forward(
         ctypes.byref(cfg), x.qk(q, cfg.q_stride), x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride),
-        x.decay(log_decay), _dense(offsets, x.i32, (x.b + 1,)), x.state(initial_state, x.b),
-        x.vo(out, cfg.out_stride), x.state(final_state, x.b), wp, wn, _stream_of(stream, v)),
+        x.decay(log_decay), x.index(offsets, x.b + 1), x.state(initial_state, x.b),
+        x.vo(out, cfg.out_stride), x.state(final_state, x.b), wp, wn, _stream_of(stream, x.dev)),
         "m3_linear_attention_forward")
 
 
 def m3_linear_attention_step(cfg: LinearAttentionConfig, q, k, v, log_decay, slots, state, out,
                              stream=None):
-    x = _LaShapes(cfg)
+    x = _LaShapes(cfg, v)
     _check(load_library().m3_linear_attention_step(
         ctypes.byref(cfg), x.qk(q, cfg.q_stride), x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride),
-        x.decay(log_decay), _dense(slots, x.i32, (x.b,)), x.state(state, cfg.num_slots or x.b),
-        x.vo(out, cfg.out_stride), _stream_of(stream, v)), "m3_linear_attention_step")
+        x.decay(log_decay), x.index(slots, x.b), x.state(state, cfg.num_slots or x.b),
+        x.vo(out, cfg.out_stride), _stream_of(stream, x.dev)), "m3_linear_attention_step")
 
 
 def m3_linear_attention_backward_workspace(cfg: LinearAttentionConfig) -> int:
@@ -632,12 +668,12 @@ def m3_linear_attention_backward_workspace(cfg: LinearAttentionConfig) -> int:
 def m3_linear_attention_backward(cfg: LinearAttentionConfig, grad_out, q, k, v, log_decay, offsets,
                                  initial_state, grad_final_state, grad_q, grad_k, grad_v,
                                  grad_initial_state, workspace=None, stream=None):
-    wp, wn = _ws(workspace)
-    x = _LaShapes(cfg)
+    x = _LaShapes(cfg, v)
+    wp, wn = _ws_on(workspace, x.dev)
     _check(load_library().m3_linear_attention_backward(
         ctypes.byref(cfg), x.vo(grad_out, cfg.out_stride), x.qk(q, cfg.q_stride),
         x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride), x.decay(log_decay),
-        _dense(offsets, x.i32, (x.b + 1,)), x.state(initial_state, x.b),
+        x.index(offsets, x.b + 1), x.state(initial_state, x.b),
         x.state(grad_final_state, x.b), x.qk(grad_q, 0), x.qk(grad_k, 0), x.vo(grad_v, 0),
-        x.state(grad_initial_state, x.b), wp, wn, _stream_of(stream, v)),
+        x.state(grad_initial_state, x.b), wp, wn, _stream_of(stream, x.dev)),
         "m3_linear_attention_backward")
