@@ -544,29 +544,30 @@ def qk_norm_rope_config(q, k, *, num_rope_angles, max_positions=0, epsilon=1e-6,
                             num_rope_angles, max_positions, *strides, epsilon, _dtype(some))
 
 
-def _rope_operands(cfg, dtype, q, k, q_stride, k_stride, dev):
-    rows, d, hq, hk = cfg.rows, cfg.head_dim, cfg.num_q_heads, cfg.num_k_heads
-    return (_act(q, dtype, rows, hq, d, q_stride, dev) if hq else None,
-            _act(k, dtype, rows, hk, d, k_stride, dev) if hk else None)
-
-
-def _rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions, dev):
-    f32, _, i32 = _torch_types()[:3]
-    d, a = (cfg.head_dim,), cfg.num_rope_angles
+def _rope_tables(cfg, types, rows, d, q_weight, k_weight, cos_table, sin_table, positions, dev):
+    f32, a = types[0], cfg.num_rope_angles
     table = (cfg.max_positions, a) if a else (0,)
-    return (_dense(q_weight, f32, d, dev), _dense(k_weight, f32, d, dev),
+    return (_dense(q_weight, f32, (d,), dev), _dense(k_weight, f32, (d,), dev),
             _dense(cos_table, f32, table, dev), _dense(sin_table, f32, table, dev),
-            _dense(positions, i32, (cfg.rows,), dev))
+            _dense(positions, types[2], (rows,), dev))
+
+
+def _rope_shapes(cfg, some):
+    """(types, activations' type, device, rows, query heads, key heads, width) of a call."""
+    types = _torch_types()
+    return (types, types[cfg.dtype], _device_of(some), cfg.rows, cfg.num_q_heads, cfg.num_k_heads,
+            cfg.head_dim)
 
 
 def m3_qk_norm_rope(cfg: QkNormRopeConfig, q, k, q_weight, k_weight, cos_table, sin_table,
                     positions, q_out, k_out, stream=None):
-    lib = load_library()
-    dt, dev = _torch_types()[cfg.dtype], _device_of(k if q is None else q)
-    _check(lib.m3_qk_norm_rope(
-        ctypes.byref(cfg), *_rope_operands(cfg, dt, q, k, cfg.q_stride, cfg.k_stride, dev),
-        *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions, dev),
-        *_rope_operands(cfg, dt, q_out, k_out, cfg.q_out_stride, cfg.k_out_stride, dev),
+    types, dt, dev, rows, hq, hk, d = _rope_shapes(cfg, k if q is None else q)
+    _check(load_library().m3_qk_norm_rope(
+        ctypes.byref(cfg), _act(q, dt, rows, hq, d, cfg.q_stride, dev) if hq else None,
+        _act(k, dt, rows, hk, d, cfg.k_stride, dev) if hk else None,
+        *_rope_tables(cfg, types, rows, d, q_weight, k_weight, cos_table, sin_table, positions, dev),
+        _act(q_out, dt, rows, hq, d, cfg.q_out_stride, dev) if hq else None,
+        _act(k_out, dt, rows, hk, d, cfg.k_out_stride, dev) if hk else None,
         _stream_of(stream, dev)), "m3_qk_norm_rope")
 
 
@@ -580,16 +581,16 @@ def m3_qk_norm_rope_backward_workspace(cfg: QkNormRopeConfig) -> int:
 def m3_qk_norm_rope_backward(cfg: QkNormRopeConfig, q, k, q_weight, k_weight, cos_table, sin_table,
                              positions, grad_q_out, grad_k_out, grad_q, grad_k, grad_q_weight,
                              grad_k_weight, workspace=None, stream=None):
-    types, dev = _torch_types(), _device_of(k if q is None else q)
-    d, dt = (cfg.head_dim,), types[cfg.dtype]
+    types, dt, dev, rows, hq, hk, d = _rope_shapes(cfg, k if q is None else q)
     wp, wn = _ws_on(workspace, dev)
+    side = lambda t, heads, stride: _act(t, dt, rows, heads, d, stride, dev) if heads else None  # noqa: E731
     _check(load_library().m3_qk_norm_rope_backward(
-        ctypes.byref(cfg), *_rope_operands(cfg, dt, q, k, cfg.q_stride, cfg.k_stride, dev),
-        *_rope_tables(cfg, q_weight, k_weight, cos_table, sin_table, positions, dev),
-        *_rope_operands(cfg, dt, grad_q_out, grad_k_out, cfg.q_out_stride, cfg.k_out_stride, dev),
-        *_rope_operands(cfg, dt, grad_q, grad_k, 0, 0, dev),
-        _dense(grad_q_weight, types[0], d, dev), _dense(grad_k_weight, types[0], d, dev), wp, wn,
-        _stream_of(stream, dev)), "m3_qk_norm_rope_backward")
+        ctypes.byref(cfg), side(q, hq, cfg.q_stride), side(k, hk, cfg.k_stride),
+        *_rope_tables(cfg, types, rows, d, q_weight, k_weight, cos_table, sin_table, positions, dev),
+        side(grad_q_out, hq, cfg.q_out_stride), side(grad_k_out, hk, cfg.k_out_stride),
+        side(grad_q, hq, 0), side(grad_k, hk, 0), _dense(grad_q_weight, types[0], (d,), dev),
+        _dense(grad_k_weight, types[0], (d,), dev), wp, wn, _stream_of(stream, dev)),
+        "m3_qk_norm_rope_backward")
 
 
 def linear_attention_config(q, k, v, *, batch_size, sequence_length, num_heads=None, num_groups=0,
@@ -603,31 +604,11 @@ def linear_attention_config(q, k, v, *, batch_size, sequence_length, num_heads=N
                                  v.shape[-1], q.shape[-1], num_slots, *strides, scale, _dtype(v))
 
 
-class _LaShapes:
-    """Checks of one call's operands against its config."""
-    __slots__ = ("dev", "dt", "f32", "i32", "b", "r", "h", "g", "n", "p")
-
-    def __init__(self, cfg, v):
-        types = _torch_types()
-        self.dev = _device_of(v)
-        self.f32, self.i32, self.dt = types[0], types[2], types[cfg.dtype]
-        self.b, self.r, self.h = cfg.batch_size, cfg.total_rows, cfg.num_heads
-        self.g, self.n, self.p = cfg.num_groups or self.h, cfg.state_size, cfg.head_dim
-
-    def qk(self, t, stride):
-        return _act(t, self.dt, self.r, self.g, self.n, stride, self.dev)
-
-    def vo(self, t, stride):
-        return _act(t, self.dt, self.r, self.h, self.p, stride, self.dev)
-
-    def state(self, t, count):
-        return _dense(t, self.f32, (count, self.h, self.p, self.n), self.dev)
-
-    def decay(self, t):
-        return _dense(t, self.f32, (self.h,), self.dev)
-
-    def index(self, t, count):
-        return _dense(t, self.i32, (count,), self.dev)
+def _la_shapes(cfg, v):
+    """(types, activations' type, device, B, rows, H, G, N, P) of a call."""
+    types, heads = _torch_types(), cfg.num_heads
+    return (types, types[cfg.dtype], _device_of(v), cfg.batch_size, cfg.total_rows, heads,
+            cfg.num_groups or heads, cfg.state_size, cfg.head_dim)
 
 
 def m3_linear_attention_forward_workspace(cfg: LinearAttentionConfig) -> int:
@@ -639,22 +620,29 @@ def m3_linear_attention_forward_workspace(cfg: LinearAttentionConfig) -> int:
 
 def m3_linear_attention_forward(cfg: LinearAttentionConfig, q, k, v, log_decay, offsets,
                                 initial_state, out, final_state, workspace=None, stream=None):
-    x = _LaShapes(cfg, v)
-    wp, wn = _ws_on(workspace, x.dev)
+    types, dt, dev, b, r, h, g, n, p = _la_shapes(cfg, v)
+    f32, state = types[0], (b, h, p, n)
+    wp, wn = _ws_on(workspace, dev)
     _check(load_library().m3_linear_attention_forward(
-        ctypes.byref(cfg), x.qk(q, cfg.q_stride), x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride),
-        x.decay(log_decay), x.index(offsets, x.b + 1), x.state(initial_state, x.b),
-        x.vo(out, cfg.out_stride), x.state(final_state, x.b), wp, wn, _stream_of(stream, x.dev)),
+        ctypes.byref(cfg), _act(q, dt, r, g, n, cfg.q_stride, dev),
+        _act(k, dt, r, g, n, cfg.k_stride, dev), _act(v, dt, r, h, p, cfg.v_stride, dev),
+        _dense(log_decay, f32, (h,), dev), _dense(offsets, types[2], (b + 1,), dev),
+        _dense(initial_state, f32, state, dev), _act(out, dt, r, h, p, cfg.out_stride, dev),
+        _dense(final_state, f32, state, dev), wp, wn, _stream_of(stream, dev)),
         "m3_linear_attention_forward")
 
 
 def m3_linear_attention_step(cfg: LinearAttentionConfig, q, k, v, log_decay, slots, state, out,
                              stream=None):
-    x = _LaShapes(cfg, v)
+    types, dt, dev, b, r, h, g, n, p = _la_shapes(cfg, v)
+    f32 = types[0]
     _check(load_library().m3_linear_attention_step(
-        ctypes.byref(cfg), x.qk(q, cfg.q_stride), x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride),
-        x.decay(log_decay), x.index(slots, x.b), x.state(state, cfg.num_slots or x.b),
-        x.vo(out, cfg.out_stride), _stream_of(stream, x.dev)), "m3_linear_attention_step")
+        ctypes.byref(cfg), _act(q, dt, r, g, n, cfg.q_stride, dev),
+        _act(k, dt, r, g, n, cfg.k_stride, dev), _act(v, dt, r, h, p, cfg.v_stride, dev),
+        _dense(log_decay, f32, (h,), dev), _dense(slots, types[2], (b,), dev),
+        _dense(state, f32, (cfg.num_slots or b, h, p, n), dev),
+        _act(out, dt, r, h, p, cfg.out_stride, dev), _stream_of(stream, dev)),
+        "m3_linear_attention_step")
 
 
 def m3_linear_attention_backward_workspace(cfg: LinearAttentionConfig) -> int:
@@ -668,12 +656,15 @@ def m3_linear_attention_backward_workspace(cfg: LinearAttentionConfig) -> int:
 def m3_linear_attention_backward(cfg: LinearAttentionConfig, grad_out, q, k, v, log_decay, offsets,
                                  initial_state, grad_final_state, grad_q, grad_k, grad_v,
                                  grad_initial_state, workspace=None, stream=None):
-    x = _LaShapes(cfg, v)
-    wp, wn = _ws_on(workspace, x.dev)
+    types, dt, dev, b, r, h, g, n, p = _la_shapes(cfg, v)
+    f32, state = types[0], (b, h, p, n)
+    wp, wn = _ws_on(workspace, dev)
     _check(load_library().m3_linear_attention_backward(
-        ctypes.byref(cfg), x.vo(grad_out, cfg.out_stride), x.qk(q, cfg.q_stride),
-        x.qk(k, cfg.k_stride), x.vo(v, cfg.v_stride), x.decay(log_decay),
-        x.index(offsets, x.b + 1), x.state(initial_state, x.b),
-        x.state(grad_final_state, x.b), x.qk(grad_q, 0), x.qk(grad_k, 0), x.vo(grad_v, 0),
-        x.state(grad_initial_state, x.b), wp, wn, _stream_of(stream, x.dev)),
+        ctypes.byref(cfg), _act(grad_out, dt, r, h, p, cfg.out_stride, dev),
+        _act(q, dt, r, g, n, cfg.q_stride, dev), _act(k, dt, r, g, n, cfg.k_stride, dev),
+        _act(v, dt, r, h, p, cfg.v_stride, dev), _dense(log_decay, f32, (h,), dev),
+        _dense(offsets, types[2], (b + 1,), dev), _dense(initial_state, f32, state, dev),
+        _dense(grad_final_state, f32, state, dev), _act(grad_q, dt, r, g, n, 0, dev),
+        _act(grad_k, dt, r, g, n, 0, dev), _act(grad_v, dt, r, h, p, 0, dev),
+        _dense(grad_initial_state, f32, state, dev), wp, wn, _stream_of(stream, dev)),
         "m3_linear_attention_backward")
