@@ -513,6 +513,23 @@ def _act(t, dtype, rows, heads, width, stride, dev):
     return t.data_ptr() if n > 0 else None
 
 
+def _ends(shape):
+    out, run = [], 1
+    for size in reversed(shape):
+        run *= size
+        out.append(run)
+    return out
+
+
+def _same_memory(shape, want):
+    """Whether a dense tensor of `shape` lies in memory as one of `want`: it may merge
+    dimensions, split the first one and have others of one value."""
+    mine, ends = _ends(shape) or [1], _ends(want)
+    inner = ends[-2] if len(ends) > 1 else 1
+    return mine[-1:] == ends[-1:] and all(
+        x == 1 or x in ends or (x > inner and (inner == 1 or inner in mine)) for x in mine)
+
+
 def _dense(t, dtype, shape, dev):
     """Device pointer of a dense operand of one type and shape (None passes NULL)."""
     if t is None:
@@ -522,13 +539,10 @@ def _dense(t, dtype, shape, dev):
             raise TypeError(f"expected a contiguous {dtype} CUDA tensor")
         raise _other_device(t, dev)
     if t.shape != shape:
-        n = 1
-        for x in shape:
-            n *= x
-        if t.numel() != n:
-            raise ValueError(f"expected a tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
-        if n == 0:
+        if t.numel() == 0 and 0 in shape:
             return None
+        if not _same_memory(t.shape, shape):
+            raise ValueError(f"expected a tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 

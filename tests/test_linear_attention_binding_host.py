@@ -108,3 +108,26 @@ def test_operands_on_a_device_that_is_not_the_current_one_are_refused(which, mad
     with pytest.raises(ValueError, match="current device"):
         call(which, device=1)
     assert not made
+
+
+@pytest.mark.parametrize("which,operand,shape", [
+    ("forward", "s0", (2, HEADS, N, P)), ("forward", "final", (HEADS, 2 * P, N // 2, 2)),
+    ("forward", "final", (2, P, N, HEADS)), ("step", "state", (HEADS, SLOTS, P, N)),
+    ("backward", "ds", (2, HEADS, N, P)), ("rope", "cos", (ANGLES, 32)),
+    ("rope_backward", "sin", (ANGLES, 2, 16))])
+def test_another_shape_of_as_many_values_is_refused(which, operand, shape, made):
+    with pytest.raises(ValueError, match="shape"):
+        call(which, **{operand: On(torch.zeros(*shape))})
+    assert not made
+
+
+@pytest.mark.parametrize("which,operand,dt,shape", [
+    ("forward", "s0", F, (2 * HEADS, P, N)), ("forward", "final", F, (2 * HEADS * P * N,)),
+    ("forward", "s0", F, (2, HEADS, P * N)), ("backward", "ds", F, (2, 1, HEADS, P, N)),
+    ("step", "state", F, (SLOTS, HEADS * P, N)), ("rope", "cos", F, (4, 8, ANGLES)),
+    ("rope", "positions", I, (2, ROWS // 2)), ("rope", "q_weight", F, (1, 1, N)),
+    ("forward", "decay", F, (1, HEADS, 1, 1)), ("forward", "decay", F, (HEADS,)), ("rope", "sin", F, (32 * ANGLES,))])
+def test_the_same_values_in_other_dimensions_pass(which, operand, dt, shape, made):
+    """Dimensions merged, split at the front, or of one value: the memory is the same."""
+    call(which, **{operand: On(torch.zeros(*shape, dtype=dt))})
+    assert len(made) == 1
