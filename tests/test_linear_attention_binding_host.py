@@ -131,3 +131,33 @@ def test_the_same_values_in_other_dimensions_pass(which, operand, dt, shape, mad
     """Dimensions merged, split at the front, or of one value: the memory is the same."""
     call(which, **{operand: On(torch.zeros(*shape, dtype=dt))})
     assert len(made) == 1
+
+
+def uneven(rows):
+    """Rows of two heads that do not lie evenly: `rows` of five, three times."""
+    return torch.zeros(3, 5, HEADS, N)[:, :rows]
+
+
+def test_rows_that_are_not_evenly_spaced_are_refused():
+    even = torch.zeros(3, 5, HEADS, N)
+    assert m3.qk_norm_rope_config(even, even, num_rope_angles=0).q_stride == HEADS * N
+    with pytest.raises(TypeError, match="evenly"):
+        m3.qk_norm_rope_config(uneven(4), even, num_rope_angles=0)
+    with pytest.raises(TypeError, match="evenly"):
+        m3.qk_norm_rope_config(even, uneven(4), num_rope_angles=0)
+    with pytest.raises(TypeError, match="evenly"):
+        m3.qk_norm_rope_config(even, even, num_rope_angles=0, k_out=uneven(4))
+    for bad in range(3):
+        qkv = [even, even, even]
+        qkv[bad] = uneven(4)
+        with pytest.raises(TypeError, match="evenly"):
+            m3.linear_attention_config(*qkv, batch_size=3, sequence_length=5)
+
+
+def test_rows_that_differ_from_the_configs_are_refused(made):
+    apart = On(torch.zeros(ROWS, 2, HEADS, N)[:, 0])  # evenly spaced, but not as the config says
+    with pytest.raises(ValueError, match="stride"):
+        call("rope", q=apart)
+    with pytest.raises(TypeError, match="evenly"):  # as many rows as the config's, unevenly
+        call("rope", q=On(torch.zeros(2, 4, HEADS, N)[:, :3]))
+    assert not made
