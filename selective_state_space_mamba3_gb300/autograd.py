@@ -21,7 +21,8 @@ per packed row.
 
 The last two are the layers' own operators (m3_qk_norm_rope,
 m3_linear_attention_forward and their adjoints); their activations may be
-float32 or bfloat16 and rows of a packed projection.
+float32 or bfloat16 and rows of a packed projection. Gradients of the decays and
+of the rotation tables are refused, and so are second derivatives.
 
 cfg is the SsmConfig dict of the C ABI (batch_size, sequence_length, num_heads,
 num_groups, head_dim, state_size, num_rope_angles, mimo_rank, has_z, has_d,

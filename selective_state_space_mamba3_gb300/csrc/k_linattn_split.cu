@@ -16,12 +16,15 @@
 // fetched into L2; K's are cut and stored as soon as K^T V^ has read the tile, those
 // of Q and V as soon as P V has.
 //
-// At N = 128, P = 64 a chunk's 138 products take some 9,000 cycles of its 19,000; the
-// rest is the cutting, for which the tiles that the products read have to be free,
-// and loads that go through what 217 KB of shared memory leave of the L1. Measured on
-// 2 x 16,384 tokens, 32 heads, 4 groups: 0.81 ms, where float32 arithmetic on the CUDA
-// cores took 4.6 ms and the bytes would take 0.10. Nothing may spill: with no L1 to
-// hold them, spilled registers cost as much as the loads they hide.
+// At N = 128, P = 64 a chunk's 180 products (48 Q K^T, 48 Q S, 42 K^T V^, 42 P V) keep
+// the tensor cores active for some 7,000 of its 17,500 cycles (4 x 2048 tokens, one
+// block an SM: 40 % of the active cycles by the counter); the rest is the cutting, for
+// which the tiles that the products read have to be free, and loads that go through
+// what 217 KB of shared memory leave of the L1. Measured on 2 x 16,384 tokens, 32
+// heads, 4 groups: 0.81 ms, where float32 arithmetic on the CUDA cores took 4.6 ms and
+// the bytes would take 0.10. At N > 64 nothing spills: with no L1 to hold them, spilled
+// registers cost as much as the loads they hide. At N <= 64 a thread spills 20 bytes,
+// and with bfloat16 operands at N > 64 12.
 #include "linattn_mma.cuh"
 
 namespace m3 {

@@ -123,8 +123,12 @@ int check_rows(const La& g, const int32_t* offsets) {
   return g.rows == (int64_t)g.B * g.L ? M3_OK : M3_ERR_INVALID_ARGUMENT;
 }
 
-// Segments a sequence is cut into: the number with the shortest pass, in chunks
-// walked one after another. The kernels have a block for every 64 output columns,
+// Segments a sequence is cut into: the number with the shortest pass, counted in
+// 128-token chunks walked one after another. That is the bfloat16 kernel's chunk; the
+// float32 one walks 112 tokens, so that a segment of one such chunk takes it two walks
+// and one of four chunks five, and bfloat16 calls that tile copies do not take run on
+// it with half the places counted here: their cuts are not the best ones (4 x 2001
+// float32 tokens of one head: 16 segments, 31 walks a sequence, 18 uncut). The kernels have a block for every 64 output columns,
 // and the SMs hold two (bfloat16) or one (float32) each. A cut call walks every
 // segment twice, the first time (states alone) in about half the time, and starts
 // two more kernels, about two chunks' time. Of numbers within 5 % of each other the
